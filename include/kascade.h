@@ -92,7 +92,9 @@ extern "C" {
 #define KASCADE_DEVERR_PREFILL_ATTN 4    /* sparse prefill: a gather or MMA stage never completed */
 #define KASCADE_DEVERR_DECODE_SELECT 5   /* decode selection: a cluster exchange never completed */
 #define KASCADE_DEVERR_DECODE_GATHER 6   /* sparse decode: a bulk-copied K or V row never arrived */
-#define KASCADE_DEVERR_INDEX_LIST 7      /* KASCADE_FLAG_CHECK_INDICES: an index input out of range or unsorted */
+#define KASCADE_DEVERR_INDEX_LIST 7      /* KASCADE_FLAG_CHECK_INDICES: an index input out of range or unsorted;
+                                            kascade_sparse_decode_q8: a list entry out of range */
+#define KASCADE_DEVERR_PAGE 8            /* 8-bit cache calls: a slot or page-table entry outside the page pool */
 
 /* Operations for kascade_workspace_bytes(). */
 #define KASCADE_OP_SELECT 0
@@ -101,6 +103,7 @@ extern "C" {
 #define KASCADE_OP_DENSE 3
 #define KASCADE_OP_REFINE 4   /* kascade_refine_select, any pool length up to N */
 #define KASCADE_OP_SELECT_VARLEN 5   /* kascade_select_varlen */
+#define KASCADE_OP_SPARSE_DECODE_Q8 6   /* kascade_sparse_decode_q8, with and without index lists */
 
 typedef struct kascade_shape {
   int32_t batch;        /* B  >= 1 */
@@ -333,6 +336,130 @@ KASCADE_API int kascade_sparse_decode_paged(const kascade_shape* shape, const vo
                                             const void* v_pages, const int32_t* page_table, int32_t page_size,
                                             int32_t max_pages, const int32_t* idx, const int32_t* head_map,
                                             void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 8-bit paged KV cache.  The pages describe no such cache; a paged cache
+ * stores the same keys in fixed-size pages (README, Kernel Benchmarks note),
+ * and at 8 bits a decode step reads half the bytes.  Four calls serve it: page
+ * tables and slots from request lengths, the append that quantises new rows,
+ * single-token attention (anchor lists or dense), and the gather that hands
+ * contiguous slabs to selection and prefill.
+ *
+ *   k_pages, v_pages  device [num_pages, Hkv, page_size, d] 8-bit values
+ *   scales            device fp32 [num_pages, Hkv, page_size / scale_block, 2]:
+ *             (K scale, V scale) of scale_block consecutive rows of a page and
+ *             kv head; a stored value stands for itself times its scale.  The
+ *             calls read any scale; kascade_q8_append writes powers of two
+ *             in [2^-100, 2^122]
+ *   page_size a power of two in [16, 4096]; scale_block a power of two in
+ *             [1, min(page_size, 256)]; num_pages Hkv page_size < 2^31
+ *
+ * No access leaves the pool or the lists: a slot or page-table entry outside
+ * [0, num_pages), or a list entry outside its row's keys, is skipped or
+ * replaced by one in range, and reported in the workspace's error word
+ * (KASCADE_DEVERR_PAGE, KASCADE_DEVERR_INDEX_LIST) if the call got a
+ * workspace; the call's results are then not valid.
+ */
+#define KASCADE_CACHE_E4M3 0   /* 8-bit floating point, 4 exponent and 3 fraction bits, no infinities */
+#define KASCADE_CACHE_INT8 1   /* whole numbers in [-127, 127] (-128 reads as such, and is never written) */
+
+typedef struct kascade_q8_cache {
+  void* k_pages;
+  void* v_pages;
+  float* scales;
+  int32_t num_pages;
+  int32_t num_kv_heads;
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t page_size;
+  int32_t scale_block;
+  int32_t type;          /* KASCADE_CACHE_* */
+} kascade_q8_cache;
+
+/*
+ * Page tables and slot maps from request lengths, on the device.  Request b
+ * holds kv_lens[b] tokens on the pages page_table[b, 0 .. ceil(kv_lens[b] / P))
+ * and adds new_lens[b] (either may be 0).  The new pages it needs are taken
+ * from free_pages in order, requests in order of b, and written to its next
+ * page_table entries; other entries are left as they were.
+ *   kv_lens, new_lens  device int32 [batch], sums in [0, 2^20]
+ *   free_pages   device int32 [num_free], pages no request holds
+ *   page_table   device int32 [batch, max_pages], read and written
+ *   kv_lens_out  device int32 [batch]: kv_lens + new_lens (a buffer that
+ *                overlaps neither; copy it over kv_lens afterwards, or use
+ *                the two in turn)
+ *   offsets      device int32 [batch + 1]: first new token of each request,
+ *                and their total
+ *   slot_map     device int32 [capacity]: slot (page P + row in the page) of
+ *                every new token, requests in order, positions ascending;
+ *                -1 from the total on (a fixed capacity serves a graph)
+ *   info         device int32 [2]: pages taken, new tokens
+ * All or nothing: a negative length, a request past max_pages pages or 2^20
+ * tokens, more than num_free pages or more than capacity tokens make the call
+ * give info = (-1, 0), kv_lens_out = kv_lens, offsets 0 and every slot -1, and
+ * leave the page table as it was.  batch <= 4096.  One launch.
+ */
+KASCADE_API int kascade_page_tables(int32_t batch, int32_t page_size, int32_t max_pages, const int32_t* kv_lens,
+                                    const int32_t* new_lens, const int32_t* free_pages, int32_t num_free,
+                                    int32_t* page_table, int32_t* kv_lens_out, int32_t* offsets, int32_t* slot_map,
+                                    int32_t capacity, int32_t* info, void* stream);
+
+/*
+ * Quantises new K and V rows into the cache.  Token t's rows, kv head h, are
+ * k + t k_token_stride + h k_head_stride (elements; strides are whole 16-byte
+ * units, so views of a fused projection serve) and go to slot slot_map[t];
+ * slot -1 skips the token.  Tokens of one block must be neighbours in the
+ * token order (up to 31 skipped ones between two of them do not matter), their
+ * slots ascending and distinct, as kascade_page_tables writes them; the rows
+ * of the block before the first of them are in use, those behind the last are
+ * not.
+ * For the new rows x of a block (per kv head, K and V apart), a the largest
+ * finite |x|: the scale becomes the smallest power of two s with a <= M s (M =
+ * 448 or 127), and not less than the block's scale if rows precede; where it
+ * grows, those rows are rounded again at the new scale.  A new value is
+ * x / s rounded to nearest, ties to even, saturated at +-M (infinities too); NaN
+ * is e4m3's NaN, and 0 in int8.
+ *   dtype  KASCADE_DTYPE_* of k and v
+ *   ws     NULL, or a workspace whose error word takes bad slots
+ */
+KASCADE_API int kascade_q8_append(const kascade_q8_cache* cache, const void* k, const void* v, int64_t k_token_stride,
+                                  int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, int32_t dtype,
+                                  int32_t num_tokens, const int32_t* slot_map, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/*
+ * The cache's rows as contiguous slabs k, v [batch, Hkv, n_ctx, d] of `dtype`
+ * (either may be NULL): what kascade_select, kascade_select_varlen,
+ * kascade_sparse_prefill and kascade_dense_ref read.  Row j of request b is
+ * written for j < kv_lens[b] (device int32 [batch], held to [0, n_ctx]; NULL:
+ * n_ctx) and left as it was from there on; value times scale in fp32, rounded
+ * once.  page_table [batch, max_pages], max_pages >= ceil(n_ctx / page_size).
+ */
+KASCADE_API int kascade_q8_gather(const kascade_q8_cache* cache, int32_t batch, int32_t n_ctx,
+                                  const int32_t* page_table, int32_t max_pages, const int32_t* kv_lens, int32_t dtype,
+                                  void* k, void* v, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * kascade_sparse_decode over the 8-bit paged cache: the attention of q over
+ * the values that the cache stands for.
+ *   kv_lens  device int32 [B], held to [0, N] (NULL: N each); a row of 0 keys
+ *            gives o = 0, lse = -inf
+ *   idx      lists in the layout of kv_len = N, as kascade_select_varlen
+ *            writes them (row b's first ceil(frac kv_lens[b]) entries are
+ *            read, in any order), or NULL for dense decode over the row's keys
+ *   head_map as for kascade_sparse_decode (ignored without lists)
+ *   ws       kascade_workspace_bytes(shape, KASCADE_OP_SPARSE_DECODE_Q8)
+ *            bytes: partial results of long lists; NULL where one CTA per
+ *            list does (the call says KASCADE_ERR_WORKSPACE otherwise)
+ * q, o: shape->dtype bf16 or fp16 (KASCADE_ERR_UNSUPPORTED for fp32).  Range
+ * checks are always on; KASCADE_FLAG_CHECK_INDICES is refused.  With
+ * KASCADE_FLAG_INPUTS_STABLE the call still waits before it reads.
+ * The V scales of the keys that one row attends over should lie within a
+ * factor of 2^24 of one another: values of blocks below that keep fewer bits.
+ */
+KASCADE_API int kascade_sparse_decode_q8(const kascade_shape* shape, const kascade_q8_cache* cache, const void* q,
+                                         const int32_t* page_table, int32_t max_pages, const int32_t* kv_lens,
+                                         const int32_t* idx, const int32_t* head_map, void* o, float* lse, void* ws,
+                                         size_t ws_bytes, void* stream);
 
 /*
  * Sparse causal prefill attention of an anchor or reuse layer (README

@@ -6,6 +6,7 @@
 #include "../../include/kascade.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "q8.cuh"
 
 namespace kascade {
 namespace {
@@ -308,6 +309,69 @@ AttnArgs attn_args(const kascade_shape* s, const void* q, const void* k, const v
   return a;
 }
 
+// ----------------------------------------------------------------- 8-bit paged cache
+
+bool pow2_in(int x, int lo, int hi) { return x >= lo && x <= hi && (x & (x - 1)) == 0; }
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+int check_cache(const kascade_q8_cache* c) {
+  if (!c) return KASCADE_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->num_kv_heads < 1 || !c->k_pages || !c->v_pages || !c->scales)
+    return KASCADE_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return KASCADE_ERR_UNSUPPORTED;
+  if (!pow2_in(c->page_size, 16, 4096)) return KASCADE_ERR_UNSUPPORTED;
+  if (!pow2_in(c->scale_block, 1, c->page_size < 256 ? c->page_size : 256)) return KASCADE_ERR_UNSUPPORTED;
+  if (c->type != KASCADE_CACHE_E4M3 && c->type != KASCADE_CACHE_INT8) return KASCADE_ERR_UNSUPPORTED;
+  // row numbers are 31-bit
+  if (c->num_kv_heads > 65535 || (int64_t)c->num_pages * c->num_kv_heads > ((1ll << 31) - 1) / c->page_size)
+    return KASCADE_ERR_UNSUPPORTED;
+  if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->scales, 8)) return KASCADE_ERR_UNSUPPORTED;
+  return KASCADE_OK;
+}
+
+Q8Cache cache_args(const kascade_q8_cache* c) {
+  Q8Cache q{};
+  q.k = static_cast<uint8_t*>(c->k_pages);
+  q.v = static_cast<uint8_t*>(c->v_pages);
+  q.scales = reinterpret_cast<float2*>(c->scales);
+  q.num_pages = c->num_pages;
+  q.Hkv = c->num_kv_heads;
+  q.D = c->head_dim;
+  q.page_shift = log2_of(c->page_size);
+  q.block_shift = log2_of(c->scale_block);
+  return q;
+}
+
+bool known_dtype(int t) { return t == KASCADE_DTYPE_BF16 || t == KASCADE_DTYPE_F32 || t == KASCADE_DTYPE_F16; }
+
+// Splits of kascade_sparse_decode_q8 over lists (or, dense, over every key)
+// and their partial results behind the workspace header.
+struct Q8Plan {
+  int per, splits;
+  float2* ml;
+  float* o;
+  size_t bytes;
+};
+Q8Plan plan_q8(const kascade_shape* s, bool dense, void* ws) {
+  Q8Plan p{};
+  const bool per_head = !dense && s->select_mode == KASCADE_SELECT_PER_HEAD;
+  const int64_t problems = (int64_t)s->batch * (per_head ? s->num_q_heads : s->num_kv_heads);
+  q8_decode_plan(problems, dense ? s->kv_len : topk_count(s->kv_len, s->topk_num, s->topk_den), &p.per, &p.splits);
+  Carver cv{static_cast<char*>(ws)};
+  cv.take<char>(kHeader);
+  if (p.splits > 1) {
+    const size_t rows = (size_t)s->batch * s->num_q_heads * p.splits;
+    p.ml = cv.take<float2>(rows);
+    p.o = cv.take<float>(rows * s->head_dim);
+  }
+  p.bytes = cv.off;
+  return p;
+}
+
 }  // namespace
 }  // namespace kascade
 
@@ -334,6 +398,11 @@ size_t kascade_workspace_bytes(const kascade_shape* s, int op) {
     }
     case KASCADE_OP_SELECT_VARLEN:
       return is_decode(s) ? plan_select(s, nullptr, true).bytes : 0;
+    case KASCADE_OP_SPARSE_DECODE_Q8: {   // covers the call with and without index lists
+      if (!is_decode(s)) return 0;
+      const size_t sparse = plan_q8(s, false, nullptr).bytes, dense = plan_q8(s, true, nullptr).bytes;
+      return sparse > dense ? sparse : dense;
+    }
     default:
       return 0;
   }
@@ -729,6 +798,147 @@ int kascade_dense_ref(const kascade_shape* s, const void* q, const void* k, cons
   a.causal = causal != 0;
   if (is_f32(s)) return cuda_status(launch_sparse_prefill_f32(a, is_f16(s), st));
   return cuda_status(launch_prefill(a, st));
+}
+
+int kascade_page_tables(int32_t batch, int32_t page_size, int32_t max_pages, const int32_t* kv_lens,
+                        const int32_t* new_lens, const int32_t* free_pages, int32_t num_free, int32_t* page_table,
+                        int32_t* kv_lens_out, int32_t* offsets, int32_t* slot_map, int32_t capacity, int32_t* info,
+                        void* stream) {
+  if (batch < 1 || max_pages < 1 || num_free < 0 || capacity < 0) return KASCADE_ERR_INVALID_ARG;
+  if (!kv_lens || !new_lens || !page_table || !kv_lens_out || !offsets || !info || (num_free && !free_pages) ||
+      (capacity && !slot_map))
+    return KASCADE_ERR_INVALID_ARG;
+  if (batch > 4096 || !pow2_in(page_size, 16, 4096)) return KASCADE_ERR_UNSUPPORTED;
+  for (const void* p : {(const void*)kv_lens, (const void*)new_lens, (const void*)free_pages, (const void*)page_table,
+                        (const void*)kv_lens_out, (const void*)offsets, (const void*)slot_map, (const void*)info})
+    if (!aligned(p, 4)) return KASCADE_ERR_UNSUPPORTED;
+  // every CTA reads the lengths: the new ones go to a buffer of their own
+  const auto overlap = [&](const int32_t* p, int64_t n, const int32_t* q, int64_t m) {
+    return (uintptr_t)p < (uintptr_t)(q + m) && (uintptr_t)q < (uintptr_t)(p + n);
+  };
+  const int32_t* ins[] = {kv_lens, new_lens};
+  for (const int32_t* in : ins)
+    if (overlap(kv_lens_out, batch, in, batch) || overlap(offsets, (int64_t)batch + 1, in, batch) ||
+        overlap(info, 2, in, batch) || (capacity && overlap(slot_map, capacity, in, batch)))
+      return KASCADE_ERR_INVALID_ARG;
+  PageTablesArgs a{};
+  a.kv_lens = kv_lens;
+  a.new_lens = new_lens;
+  a.free_pages = free_pages;
+  a.page_table = page_table;
+  a.lens_out = kv_lens_out;
+  a.offsets = offsets;
+  a.slot_map = slot_map;
+  a.info = info;
+  a.B = batch;
+  a.page_shift = log2_of(page_size);
+  a.max_pages = max_pages;
+  a.num_free = num_free;
+  a.capacity = capacity;
+  return cuda_status(launch_page_tables(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kascade_q8_append(const kascade_q8_cache* c, const void* k, const void* v, int64_t k_token_stride,
+                      int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, int32_t dtype,
+                      int32_t num_tokens, const int32_t* slot_map, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_cache(c);
+  if (rc) return rc;
+  if (num_tokens < 0) return KASCADE_ERR_INVALID_ARG;
+  if (!known_dtype(dtype)) return KASCADE_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return KASCADE_OK;
+  if (!k || !v || !slot_map) return KASCADE_ERR_INVALID_ARG;
+  const int64_t unit = dtype == KASCADE_DTYPE_F32 ? 4 : 8;   // elements of 16 bytes
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4) || k_token_stride % unit || k_head_stride % unit ||
+      v_token_stride % unit || v_head_stride % unit)
+    return KASCADE_ERR_UNSUPPORTED;
+  Q8AppendArgs a{};
+  a.c = cache_args(c);
+  a.k = k;
+  a.v = v;
+  a.k_token = k_token_stride;
+  a.k_head = k_head_stride;
+  a.v_token = v_token_stride;
+  a.v_head = v_head_stride;
+  a.slots = slot_map;
+  a.T = num_tokens;
+  a.err = err_word(ws, ws_bytes);
+  return cuda_status(launch_q8_append(a, dtype, c->type, static_cast<cudaStream_t>(stream)));
+}
+
+int kascade_q8_gather(const kascade_q8_cache* c, int32_t batch, int32_t n_ctx, const int32_t* page_table,
+                      int32_t max_pages, const int32_t* kv_lens, int32_t dtype, void* k, void* v, void* ws,
+                      size_t ws_bytes, void* stream) {
+  int rc = check_cache(c);
+  if (rc) return rc;
+  if (batch < 1 || n_ctx < 1 || !page_table || (!k && !v)) return KASCADE_ERR_INVALID_ARG;
+  if (!known_dtype(dtype) || n_ctx > (1 << 20)) return KASCADE_ERR_UNSUPPORTED;
+  if (max_pages < (n_ctx + c->page_size - 1) / c->page_size) return KASCADE_ERR_INVALID_ARG;
+  if (!aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(k, 16) || !aligned(v, 16))
+    return KASCADE_ERR_UNSUPPORTED;
+  // (a CTA takes at least 32 rows of one slab)
+  if ((int64_t)batch * c->num_kv_heads > ((1ll << 31) - 1) / (n_ctx / 32 + 1)) return KASCADE_ERR_UNSUPPORTED;
+  Q8GatherArgs a{};
+  a.c = cache_args(c);
+  a.page_table = page_table;
+  a.kv_lens = kv_lens;
+  a.k = k;
+  a.v = v;
+  a.B = batch;
+  a.N = n_ctx;
+  a.max_pages = max_pages;
+  a.err = err_word(ws, ws_bytes);
+  return cuda_status(launch_q8_gather(a, dtype, c->type, static_cast<cudaStream_t>(stream)));
+}
+
+int kascade_sparse_decode_q8(const kascade_shape* s, const kascade_q8_cache* c, const void* q,
+                             const int32_t* page_table, int32_t max_pages, const int32_t* kv_lens, const int32_t* idx,
+                             const int32_t* head_map, void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_shape(s);
+  if (rc) return rc;
+  rc = check_cache(c);
+  if (rc) return rc;
+  if (!is_decode(s) || s->dtype == KASCADE_DTYPE_F32 || checking(s)) return KASCADE_ERR_UNSUPPORTED;
+  if (c->num_kv_heads != s->num_kv_heads || c->head_dim != s->head_dim) return KASCADE_ERR_INVALID_ARG;
+  if (!q || !o || !page_table) return KASCADE_ERR_INVALID_ARG;
+  if (max_pages < (s->kv_len + c->page_size - 1) / c->page_size) return KASCADE_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(idx, 4) ||
+      !aligned(head_map, 4) || !aligned(lse, 4))
+    return KASCADE_ERR_UNSUPPORTED;
+  Q8Plan pl = plan_q8(s, idx == nullptr, nullptr);
+  if (pl.splits > 1) {
+    rc = check_ws(ws, ws_bytes, pl.bytes);
+    if (rc) return rc;
+    pl = plan_q8(s, idx == nullptr, ws);
+  }
+  const AttnArgs t = attn_args(s, q, c->k_pages, c->v_pages, idx, head_map, o, lse);
+  if ((int64_t)t.B * t.Hp * (pl.splits > t.G ? pl.splits : t.G) > (1ll << 31) - 1) return KASCADE_ERR_UNSUPPORTED;
+  Q8DecodeArgs a{};
+  a.c = cache_args(c);
+  a.q = q;
+  a.page_table = page_table;
+  a.kv_lens = kv_lens;
+  a.idx = idx;
+  a.head_map = head_map;
+  a.o = o;
+  a.lse = lse;
+  a.part_ml = pl.ml;
+  a.part_o = pl.o;
+  a.err = err_word(ws, ws_bytes);
+  a.B = t.B;
+  a.Hq = t.Hq;
+  a.Hp = t.Hp;
+  a.G = t.G;
+  a.Gkv = t.Gkv;
+  a.N = t.N;
+  a.num = t.num;
+  a.den = t.den;
+  a.n_lists = t.n_lists;
+  a.max_pages = max_pages;
+  a.one_list = t.one_list;
+  a.per = pl.per;
+  a.splits = pl.splits;
+  a.flags = s->flags;
+  return cuda_status(launch_q8_decode(a, s->dtype, c->type, static_cast<cudaStream_t>(stream)));
 }
 
 int kascade_workspace_error(const void* ws, int* error_out, int clear, void* stream) {

@@ -1,0 +1,65 @@
+// Index arithmetic of the 8-bit paged cache: plain functions for the kernels
+// and for host code, with no CUDA dependency, so that their bounds are tested
+// on the CPU.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__CUDACC__)
+#define Q8_HD __host__ __device__ __forceinline__
+#else
+#define Q8_HD inline
+#endif
+
+namespace kascade {
+
+// A page-table entry as a page of the pool: itself, or 0 with `bad` set.
+Q8_HD uint32_t q8_page(int32_t entry, int32_t num_pages, bool& bad) {
+  if ((uint32_t)entry < (uint32_t)num_pages) return (uint32_t)entry;
+  bad = true;
+  return 0;
+}
+
+// A list entry as one of the row's n >= 1 keys: itself, or the nearest with `bad` set.
+Q8_HD int32_t q8_key(int32_t key, int32_t n, bool& bad) {
+  if ((uint32_t)key < (uint32_t)n) return key;
+  bad = true;
+  return key < 0 ? 0 : n - 1;
+}
+
+// Whether a slot lies in the pool (slot -1, a padding token, does not).
+Q8_HD bool q8_slot_ok(int32_t slot, int32_t num_pages, int page_shift) {
+  return (uint32_t)slot < ((uint32_t)num_pages << page_shift);
+}
+
+// Row of kv head h at row `in_page` of `page`: below num_pages Hkv P < 2^31.
+Q8_HD uint32_t q8_row(uint32_t page, uint32_t in_page, uint32_t h, uint32_t Hkv, int page_shift) {
+  return ((page * Hkv + h) << page_shift) + in_page;
+}
+
+// Last b with pre[b] <= x, for pre[0] = 0 <= x < pre[n]: of requests that
+// share a first element, the one that is not empty.
+Q8_HD int q8_owner(const int* pre, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Exponent of a block's scale: the smallest e with amax <= top 2^e, top =
+// 448 = 1.75 2^8 (e4m3) or 127 = 1.984375 2^6 (int8), from the bits of amax
+// (finite, >= 0), held in [-100, 122] so that 2^e and 2^-e are normal.
+// Powers of two make x / s exact, so a new row is rounded once, and a block
+// whose scale grows keeps its e4m3 rows exactly unless they turn subnormal.
+constexpr int kScaleMinExp = -100, kScaleMaxExp = 122;
+Q8_HD int q8_scale_exp(uint32_t amax_bits, bool int8) {
+  const uint32_t top_frac = int8 ? 0x7e0000u : 0x600000u;
+  const int top_exp = int8 ? 6 : 8;
+  const int e = (int)(amax_bits >> 23) - 127 - top_exp + ((amax_bits & 0x7fffffu) > top_frac ? 1 : 0);
+  return e < kScaleMinExp ? kScaleMinExp : e > kScaleMaxExp ? kScaleMaxExp : e;
+}
+
+}  // namespace kascade

@@ -16,17 +16,21 @@ __all__ = ["Shape", "KascadeError", "lib", "OP_SELECT", "OP_SPARSE_DECODE", "OP_
            "OP_DENSE", "workspace_bytes", "index_count", "index_offsets", "Workspace", "select",
            "sparse_decode", "sparse_prefill", "dense_ref", "status_str", "launch_count", "EXPORTS", "LIB_PATH",
            "select_decode_static", "select_decode_static_error", "refine_select", "OP_REFINE",
-           "index_overlap", "plan_anchors", "sparse_decode_paged", "select_varlen", "sparse_decode_varlen"]
+           "index_overlap", "plan_anchors", "sparse_decode_paged", "select_varlen", "sparse_decode_varlen",
+           "Q8Cache", "page_tables", "q8_append", "q8_gather", "sparse_decode_q8", "OP_SPARSE_DECODE_Q8",
+           "CACHE_E4M3", "CACHE_INT8"]
 
 LIB_PATH = os.environ.get("KASCADE_LIB") or os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkascade.so")
 
 OP_SELECT, OP_SPARSE_DECODE, OP_SPARSE_PREFILL, OP_DENSE, OP_REFINE, OP_SELECT_VARLEN = 0, 1, 2, 3, 4, 5
+OP_SPARSE_DECODE_Q8 = 6
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TOO_LARGE = 0, 1, 2, 3, 4, 5
 FLAG_PDL, FLAG_INPUTS_STABLE, FLAG_CHECK_INDICES, FLAG_TEST_DROP_LOAD = 1, 2, 4, 1 << 30
 DEVERR_SCORE_POOL, DEVERR_DECODE_MERGE, DEVERR_PREFILL_ATTN, DEVERR_DECODE_SELECT = 2, 3, 4, 5
-DEVERR_DECODE_GATHER, DEVERR_INDEX_LIST = 6, 7
+DEVERR_DECODE_GATHER, DEVERR_INDEX_LIST, DEVERR_PAGE = 6, 7, 8
 SELECT_GQA, SELECT_PER_HEAD, SELECT_ALL_HEADS = 0, 1, 2
 DTYPE_BF16, DTYPE_F32, DTYPE_F16 = 0, 1, 2
+CACHE_E4M3, CACHE_INT8 = 0, 1
 
 EXPORTS = ("kascade_workspace_bytes", "kascade_index_count", "kascade_index_offsets",
            "kascade_workspace_init", "kascade_select", "kascade_sparse_decode",
@@ -34,7 +38,8 @@ EXPORTS = ("kascade_workspace_bytes", "kascade_index_count", "kascade_index_offs
            "kascade_status_str", "kascade_select_decode_static", "kascade_select_decode_static_max_bytes",
            "kascade_launch_count", "kascade_select_decode_static_error", "kascade_refine_select",
            "kascade_index_overlap", "kascade_plan_anchors", "kascade_sparse_decode_paged",
-           "kascade_select_varlen", "kascade_sparse_decode_varlen")
+           "kascade_select_varlen", "kascade_sparse_decode_varlen", "kascade_page_tables", "kascade_q8_append",
+           "kascade_q8_gather", "kascade_sparse_decode_q8")
 
 
 class KascadeError(RuntimeError):
@@ -69,6 +74,13 @@ class Shape(ctypes.Structure):
         return self.q_len == 1
 
 
+class _Q8CacheArgs(ctypes.Structure):
+    """kascade_q8_cache."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("scale_block", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is missing: build it with "
@@ -100,6 +112,15 @@ def _load():
     so.kascade_sparse_decode_paged.argtypes = [SP, P, P, P, P, ctypes.c_int32, ctypes.c_int32, P, P, P, P, P,
                                                ctypes.c_size_t, P]
     so.kascade_sparse_decode_paged.restype = ctypes.c_int
+    I, L, CP = ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(_Q8CacheArgs)
+    so.kascade_page_tables.argtypes = [I, I, I, P, P, P, I, P, P, P, P, I, P, P]
+    so.kascade_page_tables.restype = ctypes.c_int
+    so.kascade_q8_append.argtypes = [CP, P, P, L, L, L, L, I, I, P, P, ctypes.c_size_t, P]
+    so.kascade_q8_append.restype = ctypes.c_int
+    so.kascade_q8_gather.argtypes = [CP, I, I, P, I, P, I, P, P, P, ctypes.c_size_t, P]
+    so.kascade_q8_gather.restype = ctypes.c_int
+    so.kascade_sparse_decode_q8.argtypes = [SP, CP, P, P, I, P, P, P, P, P, P, ctypes.c_size_t, P]
+    so.kascade_sparse_decode_q8.restype = ctypes.c_int
     so.kascade_index_overlap.argtypes = [SP, P, P, P, P]
     so.kascade_index_overlap.restype = ctypes.c_int
     so.kascade_plan_anchors.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.c_int32, ctypes.c_int32,
@@ -344,4 +365,188 @@ def dense_ref(shape: Shape, q, k, v, causal=True, o=None, lse=None, ws=None, str
     p, n = _ws(ws, shape, OP_DENSE)
     _check(lib.kascade_dense_ref(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), int(bool(causal)), _ptr(o),
                                  _ptr(lse), p, n, _stream(stream)), "kascade_dense_ref")
+    return o
+
+
+# ---------------------------------------------------------------- 8-bit paged cache
+
+_CACHE_TYPES = {torch.float8_e4m3fn: CACHE_E4M3, torch.int8: CACHE_INT8}
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32, torch.float16: DTYPE_F16}
+
+
+def _need(ok, where: str, status: int = ERR_INVALID_ARG):
+    if not ok:
+        raise KascadeError(status, where)
+
+
+def _dense(t, dtype, shape, device, where: str):
+    """t's address; raises unless t is a contiguous tensor of this type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise KascadeError(ERR_INVALID_ARG, where)
+    return t.data_ptr()
+
+
+class _On:
+    """The device and stream of a call: makes `device` the current one and an
+    explicit `stream` torch's current stream, so that what the call allocates
+    belongs to the stream that its kernels run on; `raw` is the handle."""
+
+    __slots__ = ("raw", "ctx")
+
+    def __init__(self, device, stream, where):
+        _need(device.type == "cuda", where)
+        if stream is None:
+            if device.index == torch.cuda.current_device():
+                self.ctx = None
+                self.raw = _stream(None)
+                return
+            self.ctx = torch.cuda.device(device)
+            self.raw = torch.cuda.current_stream(device).cuda_stream
+            return
+        if isinstance(stream, int):
+            # (0 is the legacy default stream, which torch's default stream is)
+            stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+        _need(stream.device == device, where)
+        self.ctx = torch.cuda.stream(stream)   # switches the device too
+        self.raw = stream.cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+class Q8Cache:
+    """An 8-bit paged KV cache: k_pages, v_pages [num_pages, Hkv, page_size, d]
+    (torch.float8_e4m3fn or torch.int8) and scales [num_pages, Hkv,
+    page_size / scale_block, 2] in fp32, the (K, V) scale of each block of rows.
+    Keeps the tensors it is given; their addresses must not change."""
+
+    def __init__(self, k_pages, v_pages, scales):
+        where = "Q8Cache"
+        _need(k_pages.dim() == 4 and scales.dim() == 4 and k_pages.dtype in _CACHE_TYPES, where)
+        n, h, page, d = k_pages.shape
+        blocks = scales.shape[2]
+        _need(n > 0 and h > 0 and page > 0 and d > 0 and blocks > 0 and page % blocks == 0, where)
+        self.device = k_pages.device
+        kp = _dense(k_pages, k_pages.dtype, (n, h, page, d), self.device, where)
+        vp = _dense(v_pages, k_pages.dtype, (n, h, page, d), self.device, where)
+        sp = _dense(scales, torch.float32, (n, h, blocks, 2), self.device, where)
+        self.k_pages, self.v_pages, self.scales = k_pages, v_pages, scales
+        self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = n, h, page, d
+        self.scale_block = page // blocks
+        self.args = _Q8CacheArgs(kp, vp, sp, n, h, d, page, self.scale_block, _CACHE_TYPES[k_pages.dtype])
+        self.ref = ctypes.byref(self.args)
+
+    @classmethod
+    def empty(cls, num_pages: int, num_kv_heads: int, head_dim: int, page_size: int = 64, scale_block: int = None,
+              dtype=torch.float8_e4m3fn, device="cuda") -> "Q8Cache":
+        """A zeroed cache; one scale pair per page unless scale_block says otherwise."""
+        block = min(page_size, 256) if scale_block is None else scale_block
+        _need(dtype in _CACHE_TYPES and block > 0 and page_size % block == 0, "Q8Cache.empty")
+        shape = (num_pages, num_kv_heads, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
+        return cls(k, v, torch.zeros(*shape[:2], page_size // block, 2, device=device))
+
+
+def page_tables(page_size: int, kv_lens, new_lens, free_pages, page_table, capacity: int, out=None, stream=None):
+    """kascade_page_tables: extends page_table [B, max_pages] in place for
+    new_lens [B] more tokens behind kv_lens [B], with pages from free_pages.
+    Returns (kv_lens_out [B], offsets [B + 1], slot_map [capacity], info [2]),
+    `out` if it is given (four buffers, none of them kv_lens)."""
+    where = "kascade_page_tables"
+    dev, i32 = page_table.device, torch.int32
+    _need(page_table.dim() == 2 and free_pages.dim() == 1, where)
+    n, width = page_table.shape
+    with _On(dev, stream, where) as raw:
+        if out is None:
+            # one allocation; the slots first, on its 16-byte aligned start
+            buf = torch.empty(capacity + 2 * n + 3, dtype=i32, device=dev)
+            out = (buf[capacity:capacity + n], buf[capacity + n:capacity + 2 * n + 1], buf[:capacity],
+                   buf[capacity + 2 * n + 1:])
+        lens_out, offsets, slot_map, info = out
+        _check(lib.kascade_page_tables(
+            n, page_size, width, _dense(kv_lens, i32, (n,), dev, where), _dense(new_lens, i32, (n,), dev, where),
+            _dense(free_pages, i32, free_pages.shape, dev, where), free_pages.shape[0],
+            _dense(page_table, i32, page_table.shape, dev, where), _dense(lens_out, i32, (n,), dev, where),
+            _dense(offsets, i32, (n + 1,), dev, where), _dense(slot_map, i32, (capacity,), dev, where), capacity,
+            _dense(info, i32, (2,), dev, where), raw), where)
+    return out
+
+
+def q8_append(cache: Q8Cache, k, v, slot_map, ws=None, stream=None):
+    """kascade_q8_append: quantises k, v [T, Hkv, d] (bf16, fp16 or fp32, any
+    strides of whole 16 bytes with the last dim dense) into the slots of
+    slot_map [T]."""
+    where = "kascade_q8_append"
+    dev = cache.device
+    t = k.shape[0]
+    shape = (t, cache.num_kv_heads, cache.head_dim)
+    ks, vs = k.stride(), v.stride()
+    _need(k.shape == shape and v.shape == shape and k.dtype is v.dtype and k.dtype in _DTYPES and k.device == dev
+          and v.device == dev, where)
+    _need(ks[2] == 1 and vs[2] == 1, where, ERR_UNSUPPORTED)
+    p, n = ws.args() if ws is not None else (None, 0)
+    with _On(dev, stream, where) as raw:
+        _check(lib.kascade_q8_append(cache.ref, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
+                                     _DTYPES[k.dtype], t, _dense(slot_map, torch.int32, (t,), dev, where), p, n, raw),
+               where)
+
+
+def q8_gather(cache: Q8Cache, page_table, n_ctx: int, kv_lens=None, k=None, v=None, dtype=None, ws=None, stream=None):
+    """kascade_q8_gather: the cache's rows as slabs (k, v) [B, Hkv, n_ctx, d].
+    Rows from kv_lens[b] on stay as they are in the given k and v, and are zero
+    in slabs that the call makes (both, of `dtype`, bf16 by default, unless one
+    of the two is given)."""
+    where = "kascade_q8_gather"
+    dev = cache.device
+    _need(page_table.dim() == 2, where)
+    b, width = page_table.shape
+    shape = (b, cache.num_kv_heads, n_ctx, cache.head_dim)
+    with _On(dev, stream, where) as raw:
+        if k is None and v is None:
+            make = torch.empty if kv_lens is None else torch.zeros
+            k, v = (make(shape, dtype=dtype or torch.bfloat16, device=dev) for _ in range(2))
+        one = (v if k is None else k).dtype
+        _need(one in _DTYPES, where)
+        p, n = ws.args() if ws is not None else (None, 0)
+        _check(lib.kascade_q8_gather(
+            cache.ref, b, n_ctx, _dense(page_table, torch.int32, page_table.shape, dev, where), width,
+            None if kv_lens is None else _dense(kv_lens, torch.int32, (b,), dev, where), _DTYPES[one],
+            None if k is None else _dense(k, one, shape, dev, where),
+            None if v is None else _dense(v, one, shape, dev, where), p, n, raw), where)
+    return k, v
+
+
+def sparse_decode_q8(shape: Shape, q, cache: Q8Cache, page_table, idx=None, head_map=None, kv_lens=None, o=None,
+                     lse=None, ws=None, stream=None):
+    """kascade_sparse_decode_q8: sparse (idx None: dense) decode of q
+    [B, Hq, 1, d] over an 8-bit paged cache, page_table [B, max_pages]."""
+    where = "kascade_sparse_decode_q8"
+    dev, i32 = cache.device, torch.int32
+    b, hq = shape.batch, shape.num_q_heads
+    dt = torch.float16 if shape.dtype == DTYPE_F16 else torch.bfloat16
+    _need(page_table.dim() == 2 and page_table.shape[0] == b, where)
+    _need(idx is None or idx.numel() == index_count(shape), where)
+    with _On(dev, stream, where) as raw:
+        if o is None:
+            o = torch.empty_like(q)
+        if ws is None:
+            ws = Workspace(shape, (OP_SPARSE_DECODE_Q8,), device=dev)
+        p, n = ws.args()
+        _need(q.numel() == b * hq * shape.head_dim and o.numel() == q.numel(), where)
+        _check(lib.kascade_sparse_decode_q8(
+            ctypes.byref(shape), cache.ref, _dense(q, dt, q.shape, dev, where),
+            _dense(page_table, i32, page_table.shape, dev, where), page_table.shape[1],
+            None if kv_lens is None else _dense(kv_lens, i32, (b,), dev, where),
+            None if idx is None else _dense(idx, i32, idx.shape, dev, where),
+            None if head_map is None else _dense(head_map, i32, (shape.n_lists,), dev, where),
+            _dense(o, dt, o.shape, dev, where),
+            None if lse is None else (_need(lse.numel() == b * hq, where),
+                                      _dense(lse, torch.float32, lse.shape, dev, where))[1],
+            p, n, raw), where)
     return o
