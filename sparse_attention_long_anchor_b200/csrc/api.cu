@@ -348,23 +348,25 @@ Q8Cache cache_args(const kascade_q8_cache* c) {
 
 bool known_dtype(int t) { return t == KASCADE_DTYPE_BF16 || t == KASCADE_DTYPE_F32 || t == KASCADE_DTYPE_F16; }
 
-// Splits of kascade_sparse_decode_q8 over lists (or, dense, over every key)
-// and their partial results behind the workspace header.
-struct Q8Plan {
-  int per, splits;
+// CTAs of kascade_sparse_decode_q8 over lists (or, dense, over every key) and
+// their partial results behind the workspace header.
+struct Q8Space {
+  Q8Plan plan;
+  int* share;
   float2* ml;
   float* o;
   size_t bytes;
 };
-Q8Plan plan_q8(const kascade_shape* s, bool dense, void* ws) {
-  Q8Plan p{};
+Q8Space plan_q8(const kascade_shape* s, bool dense, void* ws) {
+  Q8Space p{};
   const bool per_head = !dense && s->select_mode == KASCADE_SELECT_PER_HEAD;
-  const int64_t problems = (int64_t)s->batch * (per_head ? s->num_q_heads : s->num_kv_heads);
-  q8_decode_plan(problems, dense ? s->kv_len : topk_count(s->kv_len, s->topk_num, s->topk_den), &p.per, &p.splits);
+  const int hp = per_head ? s->num_q_heads : s->num_kv_heads;
+  p.plan = q8_decode_plan((int64_t)s->batch * hp, dense ? s->kv_len : topk_count(s->kv_len, s->topk_num, s->topk_den));
   Carver cv{static_cast<char*>(ws)};
   cv.take<char>(kHeader);
-  if (p.splits > 1) {
-    const size_t rows = (size_t)s->batch * s->num_q_heads * p.splits;
+  if (p.plan.parts) {
+    const size_t rows = (size_t)p.plan.parts * (s->num_q_heads / hp);
+    p.share = cv.take<int>(1);
     p.ml = cv.take<float2>(rows);
     p.o = cv.take<float>(rows * s->head_dim);
   }
@@ -904,14 +906,16 @@ int kascade_sparse_decode_q8(const kascade_shape* s, const kascade_q8_cache* c, 
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(idx, 4) ||
       !aligned(head_map, 4) || !aligned(lse, 4))
     return KASCADE_ERR_UNSUPPORTED;
-  Q8Plan pl = plan_q8(s, idx == nullptr, nullptr);
-  if (pl.splits > 1) {
+  Q8Space pl = plan_q8(s, idx == nullptr, nullptr);
+  if (pl.plan.parts) {
     rc = check_ws(ws, ws_bytes, pl.bytes);
     if (rc) return rc;
     pl = plan_q8(s, idx == nullptr, ws);
   }
   const AttnArgs t = attn_args(s, q, c->k_pages, c->v_pages, idx, head_map, o, lse);
-  if ((int64_t)t.B * t.Hp * (pl.splits > t.G ? pl.splits : t.G) > (1ll << 31) - 1) return KASCADE_ERR_UNSUPPORTED;
+  // grids, and the tiles of all problems, are numbered in 31 bits
+  if ((int64_t)t.B * t.Hq > (1ll << 30) || (int64_t)t.B * t.Hp > ((1ll << 31) - 1) / pl.plan.longest)
+    return KASCADE_ERR_UNSUPPORTED;
   Q8DecodeArgs a{};
   a.c = cache_args(c);
   a.q = q;
@@ -932,11 +936,14 @@ int kascade_sparse_decode_q8(const kascade_shape* s, const kascade_q8_cache* c, 
   a.N = t.N;
   a.num = t.num;
   a.den = t.den;
+  a.stride = idx ? topk_count(t.N, t.num, t.den) : t.N;
+  a.den_inv = ~0ull / (uint32_t)t.den + 1;
   a.n_lists = t.n_lists;
   a.max_pages = max_pages;
   a.one_list = t.one_list;
-  a.per = pl.per;
-  a.splits = pl.splits;
+  a.share = pl.share;
+  a.longest = pl.plan.longest;
+  a.ctas = (int)pl.plan.ctas;
   a.flags = s->flags;
   return cuda_status(launch_q8_decode(a, s->dtype, c->type, static_cast<cudaStream_t>(stream)));
 }

@@ -39,10 +39,9 @@ template <int CT>
 __device__ __forceinline__ void q8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (CT == kE4M3) {
     // every e4m3 value is an fp16 value; the conversion is one instruction
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    lo = (uint32_t)a.x | ((uint32_t)a.y << 16);
-    hi = (uint32_t)b.x | ((uint32_t)b.y << 16);
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   } else {
     // x + 128 in the low bits of fp16 1024 (spacing 1 there), less 1152
     const uint32_t u = w ^ 0x80808080u;
@@ -121,16 +120,27 @@ struct Q8DecodeArgs {
   const int32_t* head_map;
   void* o;
   float* lse;                  // may be NULL
-  float2* part_ml;             // [problem, split, G] (max, sum)
-  float* part_o;               // [problem, split, G, D]
+  float2* part_ml;             // [part, G] (max, sum)
+  float* part_o;               // [part, G, D]
+  int* share;                  // the tiles of a CTA that the lengths gave
   int* err;
   int B, Hq, Hp, G, Gkv, N, num, den, n_lists, max_pages;
+  int stride;                  // entries of a list (dense: N)
+  uint64_t den_inv;            // floor((2^64 - 1) / den) + 1
   bool one_list;
-  int per, splits;             // keys of a split (a multiple of 16), splits of a problem
+  int longest;                 // tiles of the longest list
+  int ctas;                    // CTAs (not of clusters)
+  int per;                     // tiles of a CTA, 0: found on the device (set at launch)
   int flags;
 };
-// keys per split and number of splits for `problems` lists of up to `count` keys
-void q8_decode_plan(int64_t problems, int count, int* per, int* splits);
+// The split of `problems` lists of up to `count` keys: tiles of the longest
+// list, CTAs, and partial results (of G heads each) that they may leave; 0: a
+// CTA per problem, and none.
+struct Q8Plan {
+  int longest;
+  int64_t ctas, parts;
+};
+Q8Plan q8_decode_plan(int64_t problems, int count);
 cudaError_t launch_q8_decode(const Q8DecodeArgs& a, int in_type, int cache_type, cudaStream_t stream);
 
 }  // namespace kascade

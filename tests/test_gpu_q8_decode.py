@@ -120,6 +120,40 @@ def test_many_splits(n, lens, frac):
     _case("int8", "fp16", 16, 2, 64, 128, 128, n, lens, frac, seed=n + 1, scale="free")
 
 
+@pytest.mark.parametrize("B,hkv,n,frac", [(40, 2, 600, None), (70, 1, 900, (40, 100)), (33, 8, 300, None),
+                                          (100, 3, 1400, None), (160, 2, 200, None), (148, 2, 260, None)])
+def test_batches_past_a_warp_of_rows_and_past_the_resident_ctas(B, hkv, n, frac):
+    """More rows than a warp counts at once; more problems than CTAs run at
+    once, with one and several CTAs to a problem; as many as they are."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, n + 1, B).tolist()
+    lens[3], lens[-1] = n, 0
+    _case("e4m3", "bf16", 2 * hkv, hkv, 64, 16, 16, n, lens, frac, seed=B)
+    _case("int8", "fp16", hkv, hkv, 128, 64, 4, n, [n] * B, frac, seed=B + 1)
+
+
+def test_rows_do_not_depend_on_how_the_batch_is_split():
+    """Each row of a ragged batch against the row alone, within both calls'
+    bounds of the oracle (the split follows the batch's lengths)."""
+    kc = _kc()
+    lens, n, hkv, d = [9000, 130, 0, 4321, 1], 9000, 2, 128
+    rows, _ = tables_for(lens, 64, 141, 400, 3)
+    cache = random_cache(kc, 400, hkv, 64, d, 64, "e4m3", 3)
+    q = torch.randn(5, 8, 1, d, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    o = kc.sparse_decode_q8(kc.Shape.make(5, 8, hkv, d, 1, n), q, cache, _i(rows), kv_lens=_i(lens))
+    hc = held(cache, "e4m3")
+    for b, m in enumerate(lens):
+        if m:
+            one = kc.Shape.make(1, 8, hkv, d, 1, m)
+            lse = torch.empty(1, 8, device="cuda")
+            alone = kc.sparse_decode_q8(one, q[b:b + 1].contiguous(), cache, _i([rows[b]]), lse=lse)
+            for x in (alone, o[b:b + 1]):
+                check_decode(b, q[b:b + 1].view(1, 8, d).double().cpu().numpy(), hc, [rows[b]], [m], None,
+                             x.view(1, 8, d).double().cpu().numpy(), lse.double().cpu().numpy(), torch.bfloat16)
+        else:
+            assert (o[b] == 0).all()
+
+
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
 @pytest.mark.parametrize("frac", [None, (25, 100)])
 def test_places_outside_the_contexts_do_not_matter(kind, frac):
