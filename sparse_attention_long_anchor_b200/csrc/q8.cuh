@@ -58,9 +58,12 @@ __device__ __forceinline__ void q8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi
 template <int CT>
 __device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d) {
   if constexpr (CT == kE4M3) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
+    uint32_t r;
+    asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
+        " mov.b32 %0, {l, h};\n}\n"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
   } else {
     auto one = [](float x) -> uint32_t {
       const int i = x == x ? __float2int_rn(fminf(fmaxf(x, -127.f), 127.f)) : 0;

@@ -127,52 +127,105 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const PageTabl
 //   if rows of the block precede the run: s = max(s_old, s), and where that
 //   grew, those rows become rn(y s_old / s);
 //   the new rows become rn(x / s).
-// Bound by HBM: each input value is read once from HBM (a second time from
-// L1/L2, once the maximum is known) and each byte written once.
+// Bound by HBM for prompts: each input value is read once from there (a second
+// time from L1 or L2, once its run's maximum is known) and each byte written
+// once.  A decode step is bound by latency.
 //
-// A CTA takes `tile` tokens of one (kv head, tensor) and owns the runs that
-// start there.  Runs of up to kShortRun rows (a decode step) go to a warp
-// each, which keeps the rows in registers; longer ones (a prompt) are done by
-// the whole CTA.
-
+// Two kernels, by the number of tokens (see run_append).  In both, a tile of
+// tokens owns the runs that start in it, and the heads of a token are worked on
+// next to one another: together they read whole stretches of memory.
 constexpr int kAppThreads = 256;
 constexpr int kAppWarps = kAppThreads / 32;
-constexpr int kShortRun = 8;
+constexpr int kShortRun = 8;   // rows of a run that a warp does alone
 constexpr int kMaxTile = 256;
+constexpr int kFewCtas = 4096;
+constexpr uint32_t kNoRow = 0xffffffffu;
+constexpr int kLook = 32;      // skipped tokens that part two runs of one block
 
-// eight consecutive input values as floats
+// eight consecutive input values, as they are and as floats
 template <int IN>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
+struct Raw8 {
+  uint4 w[IN == kInF32 ? 2 : 1];
+};
+template <int IN>
+__device__ __forceinline__ Raw8<IN> load8(const void* p, int64_t i) {
+  Raw8<IN> r;
   if constexpr (IN == kInF32) {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = __ldg(f), b = __ldg(f + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    const uint4* f = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+    r.w[0] = __ldg(f);
+    r.w[1] = __ldg(f + 1);
   } else {
-    const uint4 r = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    r.w[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+  }
+  return r;
+}
+template <int IN>
+__device__ __forceinline__ void floats(const Raw8<IN>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (IN == kInBf16) {
-        x[2 * j] = bf16_lo(w[j]);
-        x[2 * j + 1] = bf16_hi(w[j]);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
-      }
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (IN == kInF32) {
+      const uint4 v = r.w[1];
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      x[j] = __uint_as_float(w[j]);
+      x[4 + j] = __uint_as_float(u[j]);
+    } else if constexpr (IN == kInBf16) {
+      x[2 * j] = bf16_lo(w[j]);
+      x[2 * j + 1] = bf16_hi(w[j]);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      x[2 * j] = f.x;
+      x[2 * j + 1] = f.y;
     }
   }
 }
 
-// bits of the largest finite magnitude (non-negative floats order like their bits)
-__device__ __forceinline__ uint32_t amax_bits(const float (&x)[8], uint32_t m) {
+// Largest magnitude of the values added.  Magnitudes order like their bits, so
+// 16-bit types take the maximum of two values at once.  add() takes infinities
+// and NaN too (they come out largest: finite() is false), add_finite() leaves
+// them out.
+template <int IN>
+struct MaxAcc {
+  uint32_t m = 0;
+  __device__ __forceinline__ void add(const Raw8<IN>& r) {
+    if constexpr (IN == kInF32) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t u = __float_as_uint(x[j]) & 0x7fffffffu;
-    m = max(m, u < 0x7f800000u ? u : 0u);
+      for (int j = 0; j < 2; ++j)
+        m = max(max(m, max(r.w[j].x & 0x7fffffffu, r.w[j].y & 0x7fffffffu)),
+                max(r.w[j].z & 0x7fffffffu, r.w[j].w & 0x7fffffffu));
+    } else {
+      m = max2(max2(m, max2(r.w[0].x & 0x7fff7fffu, r.w[0].y & 0x7fff7fffu)),
+               max2(r.w[0].z & 0x7fff7fffu, r.w[0].w & 0x7fff7fffu));
+    }
   }
-  return m;
-}
+  __device__ __forceinline__ void add_finite(const Raw8<IN>& r) {
+    float x[8];
+    floats<IN>(r, x);
+    uint32_t f = 0;   // as fp32
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t u = __float_as_uint(x[j]) & 0x7fffffffu;
+      f = max(f, u < 0x7f800000u ? u : 0u);
+    }
+    if constexpr (IN == kInF32) m = max(m, f);
+    if constexpr (IN == kInBf16) m = max2(m, f >> 16);
+    if constexpr (IN == kInF16) m = max2(m, (uint32_t)__half_as_ushort(__float2half_rn(__uint_as_float(f))));
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ __forceinline__ uint32_t top() const { return IN == kInF32 ? m : max(m & 0xffffu, m >> 16); }
+  __device__ __forceinline__ bool finite() const {
+    return top() < (IN == kInF32 ? 0x7f800000u : IN == kInBf16 ? 0x7f80u : 0x7c00u);
+  }
+  __device__ __forceinline__ uint32_t bits() const {   // of the fp32 value
+    if constexpr (IN == kInF32) return m;
+    if constexpr (IN == kInBf16) return top() << 16;
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top())));
+  }
+};
 
 // x s and x / s to 24 bits, rounded to odd (towards zero, the last bit set
 // where something was dropped): rounding that to at most 8 bits then gives
@@ -193,18 +246,22 @@ __device__ __forceinline__ float div_odd(float x, float s) {
 
 // rn(x / s).  For a power of two the product with 1 / s is the quotient; a
 // block that keeps a scale of the caller's own may have any other.
-template <int CT>
-__device__ __forceinline__ uint2 pack8(const float (&x)[8], float s) {
-  float y[8];
-  if ((__float_as_uint(s) & 0x7fffffu) == 0) {
-    const float inv = 1.0f / s;
+__device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
+template <int IN, int CT>
+__device__ __forceinline__ uint2 pack8_pow2(const Raw8<IN>& r, float inv) {
+  float x[8];
+  floats<IN>(r, x);
+  return make_uint2(q8_pack4<CT>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                    q8_pack4<CT>(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+}
+template <int IN, int CT>
+__device__ __forceinline__ uint2 pack8(const Raw8<IN>& r, float s) {
+  if (is_pow2(s)) return pack8_pow2<IN, CT>(r, 1.0f / s);
+  float x[8];
+  floats<IN>(r, x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = x[j] * inv;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = div_odd(x[j], s);
-  }
-  return make_uint2(q8_pack4<CT>(y[0], y[1], y[2], y[3]), q8_pack4<CT>(y[4], y[5], y[6], y[7]));
+  for (int j = 0; j < 8; ++j) x[j] = div_odd(x[j], s);
+  return make_uint2(q8_pack4<CT>(x[0], x[1], x[2], x[3]), q8_pack4<CT>(x[4], x[5], x[6], x[7]));
 }
 
 // rn(y r) of sixteen bytes
@@ -223,33 +280,48 @@ __device__ __forceinline__ uint4 requant16(uint4 y, float r) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// What both kernels know of their (kv head, tensor).
 template <int D, int IN, int CT>
-__global__ void __launch_bounds__(kAppThreads) q8_append_kernel(const Q8AppendArgs a, int tile) {
-  constexpr int LPR = D / 8;           // lanes per input row
-  constexpr int RPW = 32 / LPR;        // input rows per warp and pass
-  constexpr int CPR = D / 16;          // 16-byte chunks per cache row
-  constexpr int PASSES = kShortRun / RPW;
-  __shared__ int long_t[kMaxTile], long_n[kMaxTile];
-  __shared__ int n_long;
-  __shared__ uint32_t red[kAppWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
-  const void* src = is_v ? a.v : a.k;
-  const int64_t ts = is_v ? a.v_token : a.k_token;
-  const int64_t hoff = (int64_t)h * (is_v ? a.v_head : a.k_head);
-  uint8_t* pages = is_v ? a.c.v : a.c.k;
-  float* scales = reinterpret_cast<float*>(a.c.scales) + (is_v ? 1 : 0);
-  const int ps = a.c.page_shift, bs = a.c.block_shift;
-  const int sub = lane / LPR, col = (lane % LPR) * 8;
-
-  auto row_of = [&](int slot) -> uint32_t {
+struct Appender {
+  static constexpr int LPR = D / 8;           // lanes per input row
+  static constexpr int RPW = 32 / LPR;        // input rows per warp and pass
+  static constexpr int CPR = D / 16;          // 16-byte chunks per cache row
+  static constexpr int STEP = kAppWarps * RPW;   // rows of the CTA's pass
+  const Q8AppendArgs& a;
+  const void* src;
+  uint8_t* pages;
+  float* scales;
+  int64_t ts, off;   // token stride; this lane's offset in a row of the head
+  int h, col;
+  // set: 0 .. Hkv - 1 the K heads, then the V heads
+  __device__ __forceinline__ Appender(const Q8AppendArgs& args, int set) : a(args) {
+    const bool is_v = set >= a.c.Hkv;
+    h = is_v ? set - a.c.Hkv : set;
+    src = is_v ? a.v : a.k;
+    pages = is_v ? a.c.v : a.c.k;
+    scales = reinterpret_cast<float*>(a.c.scales) + (is_v ? 1 : 0);
+    ts = is_v ? a.v_token : a.k_token;
+    col = (threadIdx.x % LPR) * 8;
+    off = (int64_t)h * (is_v ? a.v_head : a.k_head) + col;
+  }
+  __device__ __forceinline__ bool valid(int slot) const { return q8_slot_ok(slot, a.c.num_pages, a.c.page_shift); }
+  __device__ __forceinline__ uint32_t block_of(int slot) const { return (uint32_t)slot >> a.c.block_shift; }
+  __device__ __forceinline__ uint32_t offset_in_block(int slot) const {
+    return (uint32_t)slot & ((1u << a.c.block_shift) - 1u);
+  }
+  __device__ __forceinline__ uint32_t row_of(int slot) const {
+    const int ps = a.c.page_shift;
     return q8_row((uint32_t)slot >> ps, (uint32_t)slot & ((1u << ps) - 1u), h, a.c.Hkv, ps);
-  };
-  auto valid = [&](int slot) { return q8_slot_ok(slot, a.c.num_pages, ps); };
-  // the block's scale once the run's maximum is known: (scale, ratio for the
-  // rows before the run, 1 when they stay)
-  auto new_scale = [&](uint32_t amax, uint32_t offset, float old, float& ratio) -> float {
+  }
+  __device__ __forceinline__ float* scale_at(uint32_t row) const { return scales + 2 * (size_t)(row >> a.c.block_shift); }
+  __device__ __forceinline__ Raw8<IN> load(int t) const { return load8<IN>(src, (int64_t)t * ts + off); }
+  __device__ __forceinline__ void store_row(uint32_t row, const Raw8<IN>& r, float s) const {
+    *reinterpret_cast<uint2*>(pages + (size_t)row * D + col) = pack8<IN, CT>(r, s);
+  }
+  __device__ __forceinline__ void store(int slot, const Raw8<IN>& r, float s) const { store_row(row_of(slot), r, s); }
+  // the block's scale once the run's maximum is known; ratio: of the rows
+  // before the run, 1 when they stay
+  __device__ __forceinline__ float new_scale(uint32_t amax, uint32_t offset, float old, float& ratio) const {
     float s = pow2f(q8_scale_exp(amax, CT == kInt8));
     ratio = 1.0f;
     if (offset > 0) {
@@ -257,116 +329,279 @@ __global__ void __launch_bounds__(kAppThreads) q8_append_kernel(const Q8AppendAr
       else if (old >= s) s = old;     // (a NaN old scale is dropped)
     }
     return s;
-  };
-  if (tid == 0) n_long = 0;
-  __syncthreads();
-
-  const int t0 = blockIdx.x * tile, t1 = min(a.T, t0 + tile);
-  for (int t = t0 + warp; t < t1; t += kAppWarps) {
-    const int slot = __ldg(a.slots + t);
-    if (!valid(slot)) {   // -1: a padding token
-      if (slot != -1 && lane == 0) raise_error(a.err, kErrPage);
-      continue;
+  }
+  // rows [row0, row0 + n) times ratio, by `step` threads
+  __device__ __forceinline__ void requant(uint32_t row0, int n, float ratio, int first, int step) const {
+    for (int c = first; c < n * CPR; c += step) {
+      uint4* p = reinterpret_cast<uint4*>(pages + (size_t)row0 * D) + c;
+      *p = requant16<CT>(*p, ratio);
     }
-    const uint32_t blk = (uint32_t)slot >> bs;
-    // the last token before this one that is not skipped, 32 back at most: in
-    // the same block, this one is inside a run that starts earlier
-    {
-      const int u = t - 1 - lane;
-      const int x = u >= 0 ? __ldg(a.slots + u) : -1;
-      const uint32_t m = __ballot_sync(0xffffffffu, valid(x));
-      if (m && __shfl_sync(0xffffffffu, (uint32_t)x >> bs, __ffs(m) - 1) == blk) continue;
-    }
-    // tokens of the run: to the last one before a token of another block or 32 skipped ones
+  }
+  // tokens of the run that starts at token t: to the last one before a token of
+  // another block or kLook skipped ones (a whole warp)
+  __device__ int run_length(int t, uint32_t blk) const {
     int n = 1;
     for (;;) {
-      const int u = t + n + lane;
-      const int x = u < a.T ? __ldg(a.slots + u) : -1;
-      const bool ok = valid(x), here = ok && ((uint32_t)x >> bs) == blk;
+      const int u = t + n + (int)(threadIdx.x & 31);
+      const int y = u < a.T ? __ldg(a.slots + u) : -1;
+      const bool ok = valid(y), here = ok && block_of(y) == blk;
       uint32_t in = __ballot_sync(0xffffffffu, here);
       const uint32_t other = __ballot_sync(0xffffffffu, ok && !here);
       if (other) in &= (other & (0u - other)) - 1u;   // up to the first of another block
       if (in) n += 32 - __clz(in);
-      if (!in || other) break;
+      if (!in || other) return n;
     }
+  }
+};
+
+// Few tokens (a decode step): a token to a warp, which looks around it.  Runs of
+// up to kShortRun rows are the warp's, kept in registers; longer ones the CTA's.
+template <int D, int IN, int CT>
+__global__ void __launch_bounds__(kAppThreads) q8_append_kernel(const Q8AppendArgs a) {
+  using A = Appender<D, IN, CT>;
+  constexpr int PASSES = kShortRun / A::RPW;
+  __shared__ int long_t[kAppWarps], long_n[kAppWarps], n_long;
+  __shared__ uint32_t red[kAppWarps];
+  const int sets = 2 * a.c.Hkv;
+  const A ap(a, blockIdx.x % sets);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane / A::LPR;
+  const int t = blockIdx.x / sets * kAppWarps + warp;
+  const int slot = t < a.T ? __ldg(a.slots + t) : -1;
+  const int back = t - 1 - lane, prev = back >= 0 && t < a.T ? __ldg(a.slots + back) : -1;
+  if (tid == 0) n_long = 0;
+  __syncthreads();
+  if (ap.valid(slot)) {
+    // a run starts here unless the last token before that is not skipped, kLook
+    // back at most, is in the same block
+    const uint32_t m = __ballot_sync(0xffffffffu, ap.valid(prev)), blk = ap.block_of(slot);
+    const bool starts = !m || __shfl_sync(0xffffffffu, ap.block_of(prev), __ffs(m) - 1) != blk;
+    const int n = starts ? ap.run_length(t, blk) : 0;
     if (n > kShortRun) {
       if (lane == 0) {
         const int i = atomicAdd(&n_long, 1);
         long_t[i] = t;
         long_n[i] = n;
       }
-      continue;
-    }
-    float x[PASSES][8];
-    int at[PASSES];
-    uint32_t am = 0;
+    } else if (n > 0) {
+      Raw8<IN> v[PASSES];
+      int at[PASSES];
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int i = p * RPW + sub;
-      at[p] = i < n ? __ldg(a.slots + t + i) : -1;
-      if (valid(at[p])) {
-        load8<IN>(src, (int64_t)(t + i) * ts + hoff + col, x[p]);
-        am = amax_bits(x[p], am);
+      for (int p = 0; p < PASSES; ++p) {
+        const int i = p * A::RPW + sub;
+        at[p] = i < n ? __ldg(a.slots + t + i) : -1;
+        if (ap.valid(at[p])) v[p] = ap.load(t + i);
       }
-    }
-    am = __reduce_max_sync(0xffffffffu, am);
-    const uint32_t offset = (uint32_t)slot & ((1u << bs) - 1u);
-    const uint32_t row = row_of(slot), row0 = row - offset;
-    float* sp = scales + 2 * (size_t)(row >> bs);
-    const float old = offset ? *sp : 0.0f;
-    float ratio;
-    const float s = new_scale(am, offset, old, ratio);
-    __syncwarp();
-    if (lane == 0) *sp = s;
-    if (ratio != 1.0f)
-      for (int c = lane; c < (int)offset * CPR; c += 32) {
-        uint4* p = reinterpret_cast<uint4*>(pages + (size_t)row0 * D) + c;
-        *p = requant16<CT>(*p, ratio);
-      }
+      MaxAcc<IN> acc;
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      if (valid(at[p]))
-        *reinterpret_cast<uint2*>(pages + (size_t)row_of(at[p]) * D + col) = pack8<CT>(x[p], s);
+      for (int p = 0; p < PASSES; ++p)
+        if (ap.valid(at[p])) acc.add_finite(v[p]);
+      const uint32_t offset = ap.offset_in_block(slot), row = ap.row_of(slot);
+      float* sp = ap.scale_at(row);
+      const float old = offset ? *sp : 0.0f;
+      const uint32_t am = __reduce_max_sync(0xffffffffu, acc.bits());
+      float ratio;
+      const float s = ap.new_scale(am, offset, old, ratio);
+      __syncwarp();
+      if (lane == 0) *sp = s;
+      if (ratio != 1.0f) ap.requant(row - offset, offset, ratio, lane, 32);
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (ap.valid(at[p])) ap.store(at[p], v[p], s);
     }
+  } else if (slot != -1 && lane == 0) {   // (-1: a padding token)
+    raise_error(a.err, kErrPage);
   }
   __syncthreads();
 
-  const int runs = n_long;
+  const int runs = n_long, i0 = warp * A::RPW + sub;
   for (int q = 0; q < runs; ++q) {
-    const int t = long_t[q], n = long_n[q];
-    uint32_t am = 0;
-    for (int i = warp * RPW + sub; i < n; i += kAppWarps * RPW) {
-      float x[8];
-      if (!valid(__ldg(a.slots + t + i))) continue;
-      load8<IN>(src, (int64_t)(t + i) * ts + hoff + col, x);
-      am = amax_bits(x, am);
-    }
-    am = __reduce_max_sync(0xffffffffu, am);
-    if (lane == 0) red[warp] = am;
-    const int slot = __ldg(a.slots + t);
-    const uint32_t offset = (uint32_t)slot & ((1u << bs) - 1u);
-    const uint32_t row = row_of(slot), row0 = row - offset;
-    float* sp = scales + 2 * (size_t)(row >> bs);
+    const int rt = long_t[q], n = long_n[q];
+    MaxAcc<IN> acc;
+    for (int i = i0; i < n; i += A::STEP)
+      if (ap.valid(__ldg(a.slots + rt + i))) acc.add_finite(ap.load(rt + i));
+    const int first = __ldg(a.slots + rt);
+    const uint32_t offset = ap.offset_in_block(first), row = ap.row_of(first);
+    float* sp = ap.scale_at(row);
     const float old = offset ? *sp : 0.0f;
+    uint32_t am = __reduce_max_sync(0xffffffffu, acc.bits());
+    if (lane == 0) red[warp] = am;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kAppWarps; ++w) am = max(am, red[w]);
     float ratio;
-    const float s = new_scale(am, offset, old, ratio);
-    if (ratio != 1.0f)
-      for (int c = tid; c < (int)offset * CPR; c += kAppThreads) {
-        uint4* p = reinterpret_cast<uint4*>(pages + (size_t)row0 * D) + c;
-        *p = requant16<CT>(*p, ratio);
-      }
-    for (int i = warp * RPW + sub; i < n; i += kAppWarps * RPW) {
-      const int sl = __ldg(a.slots + t + i);
-      if (!valid(sl)) continue;
-      float x[8];
-      load8<IN>(src, (int64_t)(t + i) * ts + hoff + col, x);
-      *reinterpret_cast<uint2*>(pages + (size_t)row_of(sl) * D + col) = pack8<CT>(x, s);
+    const float s = ap.new_scale(am, offset, old, ratio);
+    if (ratio != 1.0f) ap.requant(row - offset, offset, ratio, tid, kAppThreads);
+    for (int i = i0; i < n; i += A::STEP) {   // (the rows come from L1 or L2)
+      const int y = __ldg(a.slots + rt + i);
+      if (ap.valid(y)) ap.store(y, ap.load(rt + i), s);
     }
     __syncthreads();   // every thread has read the old scale (and red) of this run
     if (tid == 0) *sp = s;
+  }
+}
+
+// Many tokens (prompts): a warp takes a tile's runs of one (kv head, tensor),
+// all at once whatever their lengths are; the CTA's warps take neighbouring
+// heads of the same tile, whose runs they find together, a token per thread.
+// Every row from the first start to the end of the last run is read and its
+// maximum joined to its run's (an integer maximum: order does not matter); a
+// lane per run finds its scale; then the rows are read again, from L1 or L2,
+// rounded and written.  What a row needs beside its values is found once per
+// CTA and kept in shared memory: instructions per value bound this kernel as
+// much as its bytes.
+template <int D, int IN, int CT>
+__global__ void __launch_bounds__(kAppThreads, 4) q8_append_tiled_kernel(const Q8AppendArgs a, int tile, int groups) {
+  using A = Appender<D, IN, CT>;
+  constexpr int kWindow = 2 * kMaxTile;          // rows looked at: a tile, and a block behind it
+  constexpr int BATCH = IN == kInF32 ? 4 : 8;    // loads of a lane under way together
+  __shared__ int sl[kLook + kWindow];            // slots of tokens t0 - kLook .. t0 + 2 tile
+  __shared__ uint32_t rows[kWindow];             // row of the token's slot for head 0, kNoRow: skipped
+  __shared__ uint32_t lead[kMaxTile / 32];       // bit x: a run starts at token t0 + x
+  __shared__ uint8_t run_id[kMaxTile];           // run of token t0 + x: the starts up to it, less 1
+  __shared__ uint32_t run_top[kAppWarps][kMaxTile];   // largest magnitude of a run, then its scale, as bits
+  __shared__ int end_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int set = blockIdx.x % groups * kAppWarps + warp;
+  const A ap(a, min(set, 2 * a.c.Hkv - 1));
+  const int t0 = blockIdx.x / groups * tile;
+  const int ps = a.c.page_shift;
+  for (int x = tid; x < kLook + 2 * tile; x += kAppThreads) {
+    const int t = t0 - kLook + x;
+    const int slot = t >= 0 && t < a.T ? __ldg(a.slots + t) : -1;
+    const bool ok = ap.valid(slot);
+    sl[x] = slot;
+    if (x >= kLook) {
+      rows[x - kLook] = ok ? q8_row((uint32_t)slot >> ps, (uint32_t)slot & ((1u << ps) - 1u), 0, a.c.Hkv, ps) : kNoRow;
+      if (slot != -1 && !ok && x < kLook + tile) raise_error(a.err, kErrPage);
+    }
+  }
+  __syncthreads();
+  if (tid < tile) {   // (tiles are whole warps)
+    bool starts = rows[tid] != kNoRow;
+    if (starts)
+      for (int k = 1; k <= kLook; ++k)
+        if (ap.valid(sl[kLook + tid - k])) {
+          starts = ap.block_of(sl[kLook + tid - k]) != ap.block_of(sl[kLook + tid]);
+          break;
+        }
+    const uint32_t m = __ballot_sync(0xffffffffu, starts);
+    if (lane == 0) lead[warp] = m;
+  }
+  __syncthreads();
+  int x_s = tile, x_l = 0, runs = 0, before = 0;   // first and last start, starts, and those of the words before this warp's
+  for (int w = 0; w < tile / 32; ++w) {
+    const uint32_t m = lead[w];
+    if (w < warp) before += __popc(m);
+    if (m) {
+      x_s = min(x_s, 32 * w + __ffs(m) - 1);
+      x_l = 32 * w + 31 - __clz(m);
+      runs += __popc(m);
+    }
+  }
+  if (runs == 0) return;
+  if (tid < tile) run_id[tid] = (uint8_t)(before + __popc(lead[warp] & (0xffffffffu >> (31 - lane))) - 1);
+  if (warp == 0) {   // the last run may end behind the tile
+    const int n = ap.run_length(t0 + x_l, ap.block_of(sl[kLook + x_l]));
+    if (lane == 0) end_s = x_l + n;
+  }
+  for (int r = lane; r < runs; r += 32) run_top[warp][r] = 0;
+  __syncthreads();
+  if (set >= 2 * a.c.Hkv) return;
+  const int end = end_s, first = x_s + lane / A::LPR;
+  const uint32_t head_row = (uint32_t)ap.h << ps;
+  // row of token t0 + x (past the window only where many are skipped)
+  auto row_at = [&](int x) -> uint32_t {
+    if (x < 2 * tile) return rows[x];
+    const int slot = __ldg(a.slots + t0 + x);
+    return ap.valid(slot) ? q8_row((uint32_t)slot >> ps, (uint32_t)slot & ((1u << ps) - 1u), 0, a.c.Hkv, ps) : kNoRow;
+  };
+  auto run_of = [&](int x) -> int { return run_id[min(x, tile - 1)]; };
+  // f(row, values, token) of every row, BATCH loads under way together
+  auto for_rows = [&](auto&& f) {
+    for (int x0 = first; x0 < end; x0 += BATCH * A::RPW) {
+      Raw8<IN> v[BATCH];
+      uint32_t r[BATCH];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        const int x = x0 + u * A::RPW;
+        r[u] = x < end ? row_at(x) : kNoRow;
+        if (r[u] != kNoRow) v[u] = ap.load(t0 + x);
+      }
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u)
+        if (r[u] != kNoRow) f(r[u], v[u], x0 + u * A::RPW);
+    }
+  };
+  // f(values, token) of every row where none is skipped: no test per row (past
+  // the end the last row again)
+  auto for_all = [&](auto&& f) {
+    for (int x0 = first; x0 < end; x0 += BATCH * A::RPW) {
+      Raw8<IN> v[BATCH];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) v[u] = ap.load(t0 + min(x0 + u * A::RPW, end - 1));
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) f(v[u], x0 + u * A::RPW);
+    }
+  };
+  // one run and no skipped row in sight: the case of a prompt
+  bool plain = runs == 1 && end <= 2 * tile;
+  for (int x = x_s + lane; plain && x < end; x += 32) plain = rows[x] != kNoRow;
+  plain = __all_sync(0xffffffffu, plain);
+  // maxima: of all rows at once, or joined row by row
+  if (plain) {
+    MaxAcc<IN> acc;
+    for_all([&](const Raw8<IN>& v, int) { acc.add(v); });
+    if (__any_sync(0xffffffffu, !acc.finite())) {
+      acc.m = 0;
+      for_rows([&](uint32_t, const Raw8<IN>& v, int) { acc.add_finite(v); });
+    }
+    const uint32_t m = __reduce_max_sync(0xffffffffu, acc.bits());
+    if (lane == 0) run_top[warp][0] = m;
+  } else {
+    for_rows([&](uint32_t, const Raw8<IN>& v, int x) {
+      MaxAcc<IN> acc;
+      acc.add(v);
+      if (!acc.finite()) {
+        acc.m = 0;
+        acc.add_finite(v);
+      }
+      atomicMax(&run_top[warp][run_of(x)], acc.bits());
+    });
+  }
+  __syncwarp();
+  // scales, a lane per run; rows before a run whose scale grew, by the warp
+  for (int x0 = 0; x0 < tile; x0 += 32) {
+    const int x = x0 + lane;
+    const bool starts = lead[x0 / 32] >> lane & 1u;
+    float ratio = 1.0f;
+    uint32_t row = 0, offset = 0;
+    if (starts) {   // token t0 + x starts a run
+      const int r = run_id[x];
+      offset = ap.offset_in_block(sl[kLook + x]);
+      row = rows[x] + head_row;
+      float* sp = ap.scale_at(row);
+      const float s = ap.new_scale(run_top[warp][r], offset, offset ? *sp : 0.0f, ratio);
+      *sp = s;
+      run_top[warp][r] = __float_as_uint(s);
+    }
+    for (uint32_t grew = __ballot_sync(0xffffffffu, ratio != 1.0f); grew; grew &= grew - 1) {
+      const int l = __ffs(grew) - 1;
+      const uint32_t n = __shfl_sync(0xffffffffu, offset, l);
+      ap.requant(__shfl_sync(0xffffffffu, row, l) - n, (int)n, __shfl_sync(0xffffffffu, ratio, l), lane, 32);
+    }
+  }
+  __syncwarp();
+  const float s0 = __uint_as_float(run_top[warp][0]);
+  if (plain && is_pow2(s0)) {
+    const float inv = 1.0f / s0;
+    for_all([&](const Raw8<IN>& v, int x) {
+      const uint2 y = pack8_pow2<IN, CT>(v, inv);
+      if (x < end) *reinterpret_cast<uint2*>(ap.pages + (size_t)(rows[x] + head_row) * D + ap.col) = y;
+    });
+  } else {
+    for_rows([&](uint32_t r, const Raw8<IN>& v, int x) {
+      ap.store_row(r + head_row, v, __uint_as_float(run_top[warp][run_of(x)]));
+    });
   }
 }
 
@@ -443,14 +678,16 @@ __global__ void __launch_bounds__(kGatThreads) q8_gather_kernel(const Q8GatherAr
 
 template <int D, int IN, int CT>
 cudaError_t run_append(const Q8AppendArgs& a, cudaStream_t st) {
-  // eight tokens per CTA (one per warp) as long as that is not many CTAs, as
-  // in a decode step; else a tile of a block's size, so that a prompt's runs
-  // start one to a CTA and few CTAs find nothing to do
-  const int64_t small = ((int64_t)a.T + kAppWarps - 1) / kAppWarps * a.c.Hkv * 2;
-  int tile = kAppWarps;
-  if (small > 4096) tile = min(max(1 << a.c.block_shift, 64), kMaxTile);
-  const dim3 grid((a.T + tile - 1) / tile, a.c.Hkv, 2);
-  return launch_ex(q8_append_kernel<D, IN, CT>, grid, dim3(kAppThreads), 0, st, false, 1, a, tile);
+  // a token per warp as long as that is not many CTAs, as in a decode step;
+  // else tiles of a block's size, so that a prompt's runs start one to a tile
+  const int sets = 2 * a.c.Hkv;
+  const int64_t few = ((int64_t)a.T + kAppWarps - 1) / kAppWarps * sets;
+  if (few <= kFewCtas)
+    return launch_ex(q8_append_kernel<D, IN, CT>, dim3((unsigned)few), dim3(kAppThreads), 0, st, false, 1, a);
+  const int tile = min(max(1 << a.c.block_shift, 64), kMaxTile), groups = (sets + kAppWarps - 1) / kAppWarps;
+  const int64_t ctas = ((int64_t)a.T + tile - 1) / tile * groups;
+  return launch_ex(q8_append_tiled_kernel<D, IN, CT>, dim3((unsigned)ctas), dim3(kAppThreads), 0, st, false, 1, a, tile,
+                   groups);
 }
 
 template <int D, int CT>

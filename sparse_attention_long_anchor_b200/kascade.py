@@ -379,45 +379,29 @@ def _need(ok, where: str, status: int = ERR_INVALID_ARG):
         raise KascadeError(status, where)
 
 
-def _dense(t, dtype, shape, device, where: str):
-    """t's address; raises unless t is a contiguous tensor of this type, shape and device."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+def _dense(t, dtype, numel, index, where: str):
+    """t's address; raises unless t is a contiguous tensor of this type and size on CUDA device `index`."""
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != index or not t.is_contiguous():
         raise KascadeError(ERR_INVALID_ARG, where)
     return t.data_ptr()
 
 
-class _On:
-    """The device and stream of a call: makes `device` the current one and an
-    explicit `stream` torch's current stream, so that what the call allocates
-    belongs to the stream that its kernels run on; `raw` is the handle."""
+def _here(index, stream):
+    """Whether a call runs as things are: on the current device and its current stream."""
+    return stream is None and index == torch.cuda.current_device()
 
-    __slots__ = ("raw", "ctx")
 
-    def __init__(self, device, stream, where):
-        _need(device.type == "cuda", where)
-        if stream is None:
-            if device.index == torch.cuda.current_device():
-                self.ctx = None
-                self.raw = _stream(None)
-                return
-            self.ctx = torch.cuda.device(device)
-            self.raw = torch.cuda.current_stream(device).cuda_stream
-            return
-        if isinstance(stream, int):
-            # (0 is the legacy default stream, which torch's default stream is)
-            stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
-        _need(stream.device == device, where)
-        self.ctx = torch.cuda.stream(stream)   # switches the device too
-        self.raw = stream.cuda_stream
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on(device, stream, where):
+    """A context in which `device` is the current one and an explicit `stream`
+    torch's current stream, so that what the call allocates belongs to the
+    stream that its kernels run on."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if isinstance(stream, int):
+        # (0 is the legacy default stream, which torch's default stream is)
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    _need(stream.device == device, where)
+    return torch.cuda.stream(stream)   # switches the device too
 
 
 class Q8Cache:
@@ -432,10 +416,11 @@ class Q8Cache:
         n, h, page, d = k_pages.shape
         blocks = scales.shape[2]
         _need(n > 0 and h > 0 and page > 0 and d > 0 and blocks > 0 and page % blocks == 0, where)
-        self.device = k_pages.device
-        kp = _dense(k_pages, k_pages.dtype, (n, h, page, d), self.device, where)
-        vp = _dense(v_pages, k_pages.dtype, (n, h, page, d), self.device, where)
-        sp = _dense(scales, torch.float32, (n, h, blocks, 2), self.device, where)
+        _need(v_pages.shape == k_pages.shape and scales.shape == (n, h, blocks, 2), where)
+        self.device, self.index = k_pages.device, k_pages.get_device()   # (index -1: not a CUDA device)
+        kp = _dense(k_pages, k_pages.dtype, n * h * page * d, self.index, where)
+        vp = _dense(v_pages, k_pages.dtype, n * h * page * d, self.index, where)
+        sp = _dense(scales, torch.float32, n * h * blocks * 2, self.index, where)
         self.k_pages, self.v_pages, self.scales = k_pages, v_pages, scales
         self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = n, h, page, d
         self.scale_block = page // blocks
@@ -459,22 +444,31 @@ def page_tables(page_size: int, kv_lens, new_lens, free_pages, page_table, capac
     Returns (kv_lens_out [B], offsets [B + 1], slot_map [capacity], info [2]),
     `out` if it is given (four buffers, none of them kv_lens)."""
     where = "kascade_page_tables"
-    dev, i32 = page_table.device, torch.int32
-    _need(page_table.dim() == 2 and free_pages.dim() == 1, where)
+    dev, i32 = page_table.get_device(), torch.int32
+    _need(page_table.dim() == 2 and dev >= 0, where)
+    if not _here(dev, stream):
+        with _on(page_table.device, stream, where):
+            return page_tables(page_size, kv_lens, new_lens, free_pages, page_table, capacity, out)
     n, width = page_table.shape
-    with _On(dev, stream, where) as raw:
-        if out is None:
-            # one allocation; the slots first, on its 16-byte aligned start
-            buf = torch.empty(capacity + 2 * n + 3, dtype=i32, device=dev)
-            out = (buf[capacity:capacity + n], buf[capacity + n:capacity + 2 * n + 1], buf[:capacity],
-                   buf[capacity + 2 * n + 1:])
+    if out is None:
+        # one allocation; the slots first, on its 16-byte aligned start
+        buf = torch.empty(capacity + 2 * n + 3, dtype=i32, device=page_table.device)
+        slot_map, lens_out, offsets, info = torch.split_with_sizes(buf, (capacity, n, n + 1, 2))
+        out = (lens_out, offsets, slot_map, info)
+        sp = buf.data_ptr()
+        lp = sp + 4 * capacity
+        op, ip = lp + 4 * n, lp + 8 * n + 4
+    else:
         lens_out, offsets, slot_map, info = out
-        _check(lib.kascade_page_tables(
-            n, page_size, width, _dense(kv_lens, i32, (n,), dev, where), _dense(new_lens, i32, (n,), dev, where),
-            _dense(free_pages, i32, free_pages.shape, dev, where), free_pages.shape[0],
-            _dense(page_table, i32, page_table.shape, dev, where), _dense(lens_out, i32, (n,), dev, where),
-            _dense(offsets, i32, (n + 1,), dev, where), _dense(slot_map, i32, (capacity,), dev, where), capacity,
-            _dense(info, i32, (2,), dev, where), raw), where)
+        lp, op = _dense(lens_out, i32, n, dev, where), _dense(offsets, i32, n + 1, dev, where)
+        sp, ip = _dense(slot_map, i32, capacity, dev, where), _dense(info, i32, 2, dev, where)
+    free = free_pages.numel()
+    status = lib.kascade_page_tables(
+        n, page_size, width, _dense(kv_lens, i32, n, dev, where), _dense(new_lens, i32, n, dev, where),
+        _dense(free_pages, i32, free, dev, where), free, _dense(page_table, i32, n * width, dev, where), lp, op, sp,
+        capacity, ip, _stream(None))
+    if status:
+        raise KascadeError(status, where)
     return out
 
 
@@ -483,18 +477,23 @@ def q8_append(cache: Q8Cache, k, v, slot_map, ws=None, stream=None):
     strides of whole 16 bytes with the last dim dense) into the slots of
     slot_map [T]."""
     where = "kascade_q8_append"
-    dev = cache.device
+    dev = cache.index
+    if dev < 0 or not _here(dev, stream):
+        _need(dev >= 0, where)
+        with _on(cache.device, stream, where):
+            return q8_append(cache, k, v, slot_map, ws)
     t = k.shape[0]
-    shape = (t, cache.num_kv_heads, cache.head_dim)
-    ks, vs = k.stride(), v.stride()
-    _need(k.shape == shape and v.shape == shape and k.dtype is v.dtype and k.dtype in _DTYPES and k.device == dev
-          and v.device == dev, where)
-    _need(ks[2] == 1 and vs[2] == 1, where, ERR_UNSUPPORTED)
+    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
+    dtype = k.dtype
+    if (k.shape != (t, cache.num_kv_heads, cache.head_dim) or v.shape != k.shape or v.dtype is not dtype
+            or dtype not in _DTYPES or k.get_device() != dev or v.get_device() != dev):
+        raise KascadeError(ERR_INVALID_ARG, where)
+    _need(kd == 1 and vd == 1, where, ERR_UNSUPPORTED)
     p, n = ws.args() if ws is not None else (None, 0)
-    with _On(dev, stream, where) as raw:
-        _check(lib.kascade_q8_append(cache.ref, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
-                                     _DTYPES[k.dtype], t, _dense(slot_map, torch.int32, (t,), dev, where), p, n, raw),
-               where)
+    status = lib.kascade_q8_append(cache.ref, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, _DTYPES[dtype], t,
+                                   _dense(slot_map, torch.int32, t, dev, where), p, n, _stream(None))
+    if status:
+        raise KascadeError(status, where)
 
 
 def q8_gather(cache: Q8Cache, page_table, n_ctx: int, kv_lens=None, k=None, v=None, dtype=None, ws=None, stream=None):
@@ -503,22 +502,27 @@ def q8_gather(cache: Q8Cache, page_table, n_ctx: int, kv_lens=None, k=None, v=No
     in slabs that the call makes (both, of `dtype`, bf16 by default, unless one
     of the two is given)."""
     where = "kascade_q8_gather"
-    dev = cache.device
-    _need(page_table.dim() == 2, where)
+    dev, i32 = cache.index, torch.int32
+    _need(page_table.dim() == 2 and dev >= 0, where)
+    if not _here(dev, stream):
+        with _on(cache.device, stream, where):
+            return q8_gather(cache, page_table, n_ctx, kv_lens, k, v, dtype, ws)
     b, width = page_table.shape
     shape = (b, cache.num_kv_heads, n_ctx, cache.head_dim)
-    with _On(dev, stream, where) as raw:
-        if k is None and v is None:
-            make = torch.empty if kv_lens is None else torch.zeros
-            k, v = (make(shape, dtype=dtype or torch.bfloat16, device=dev) for _ in range(2))
-        one = (v if k is None else k).dtype
-        _need(one in _DTYPES, where)
-        p, n = ws.args() if ws is not None else (None, 0)
-        _check(lib.kascade_q8_gather(
-            cache.ref, b, n_ctx, _dense(page_table, torch.int32, page_table.shape, dev, where), width,
-            None if kv_lens is None else _dense(kv_lens, torch.int32, (b,), dev, where), _DTYPES[one],
-            None if k is None else _dense(k, one, shape, dev, where),
-            None if v is None else _dense(v, one, shape, dev, where), p, n, raw), where)
+    if k is None and v is None:
+        make = torch.empty if kv_lens is None else torch.zeros
+        k, v = (make(shape, dtype=dtype or torch.bfloat16, device=cache.device) for _ in range(2))
+    one = (v if k is None else k).dtype
+    _need(one in _DTYPES and (k is None or k.shape == shape) and (v is None or v.shape == shape), where)
+    total = b * shape[1] * n_ctx * shape[3]
+    p, n = ws.args() if ws is not None else (None, 0)
+    status = lib.kascade_q8_gather(
+        cache.ref, b, n_ctx, _dense(page_table, i32, b * width, dev, where), width,
+        None if kv_lens is None else _dense(kv_lens, i32, b, dev, where), _DTYPES[one],
+        None if k is None else _dense(k, one, total, dev, where),
+        None if v is None else _dense(v, one, total, dev, where), p, n, _stream(None))
+    if status:
+        raise KascadeError(status, where)
     return k, v
 
 
@@ -527,26 +531,29 @@ def sparse_decode_q8(shape: Shape, q, cache: Q8Cache, page_table, idx=None, head
     """kascade_sparse_decode_q8: sparse (idx None: dense) decode of q
     [B, Hq, 1, d] over an 8-bit paged cache, page_table [B, max_pages]."""
     where = "kascade_sparse_decode_q8"
-    dev, i32 = cache.device, torch.int32
+    dev, i32 = cache.index, torch.int32
+    if dev < 0 or not _here(dev, stream):
+        _need(dev >= 0, where)
+        with _on(cache.device, stream, where):
+            return sparse_decode_q8(shape, q, cache, page_table, idx, head_map, kv_lens, o, lse, ws)
     b, hq = shape.batch, shape.num_q_heads
+    n_q = b * hq * shape.head_dim
     dt = torch.float16 if shape.dtype == DTYPE_F16 else torch.bfloat16
-    _need(page_table.dim() == 2 and page_table.shape[0] == b, where)
-    _need(idx is None or idx.numel() == index_count(shape), where)
-    with _On(dev, stream, where) as raw:
-        if o is None:
-            o = torch.empty_like(q)
-        if ws is None:
-            ws = Workspace(shape, (OP_SPARSE_DECODE_Q8,), device=dev)
-        p, n = ws.args()
-        _need(q.numel() == b * hq * shape.head_dim and o.numel() == q.numel(), where)
-        _check(lib.kascade_sparse_decode_q8(
-            ctypes.byref(shape), cache.ref, _dense(q, dt, q.shape, dev, where),
-            _dense(page_table, i32, page_table.shape, dev, where), page_table.shape[1],
-            None if kv_lens is None else _dense(kv_lens, i32, (b,), dev, where),
-            None if idx is None else _dense(idx, i32, idx.shape, dev, where),
-            None if head_map is None else _dense(head_map, i32, (shape.n_lists,), dev, where),
-            _dense(o, dt, o.shape, dev, where),
-            None if lse is None else (_need(lse.numel() == b * hq, where),
-                                      _dense(lse, torch.float32, lse.shape, dev, where))[1],
-            p, n, raw), where)
+    _need(page_table.dim() == 2, where)
+    width = page_table.shape[1]
+    qp = _dense(q, dt, n_q, dev, where)
+    if o is None:
+        o = torch.empty_like(q)
+        op = o.data_ptr()
+    else:
+        op = _dense(o, dt, n_q, dev, where)
+    p, n = (Workspace(shape, (OP_SPARSE_DECODE_Q8,), device=cache.device) if ws is None else ws).args()
+    status = lib.kascade_sparse_decode_q8(
+        ctypes.byref(shape), cache.ref, qp, _dense(page_table, i32, b * width, dev, where), width,
+        None if kv_lens is None else _dense(kv_lens, i32, b, dev, where),
+        None if idx is None else _dense(idx, i32, index_count(shape), dev, where),
+        None if head_map is None else _dense(head_map, i32, shape.n_lists, dev, where), op,
+        None if lse is None else _dense(lse, torch.float32, b * hq, dev, where), p, n, _stream(None))
+    if status:
+        raise KascadeError(status, where)
     return o
