@@ -606,6 +606,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
       }
       return;
     }
+    __syncwarp();   // (converged for the aligned barrier)
     // each unit goes to the CTA that owns it, each head's (max, sum) to every CTA
     cluster_wait_acquire();   // every CTA's mbarrier is initialised
     const uint32_t recv_ml = smem_u32(smem) + (uint32_t)L::recv_ml, recv_o = smem_u32(smem) + (uint32_t)L::recv_o;

@@ -387,8 +387,11 @@ def _dense(t, dtype, numel, index, where: str):
 
 
 def _here(index, stream):
-    """Whether a call runs as things are: on the current device and its current stream."""
-    return stream is None and index == torch.cuda.current_device()
+    """The handle of the stream of a call that runs as things are, on the
+    current device `index` and its current stream; None if it does not."""
+    if stream is not None or index < 0 or index != torch.cuda.current_device():
+        return None
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def _on(device, stream, where):
@@ -446,7 +449,8 @@ def page_tables(page_size: int, kv_lens, new_lens, free_pages, page_table, capac
     where = "kascade_page_tables"
     dev, i32 = page_table.get_device(), torch.int32
     _need(page_table.dim() == 2 and dev >= 0, where)
-    if not _here(dev, stream):
+    raw = _here(dev, stream)
+    if raw is None:
         with _on(page_table.device, stream, where):
             return page_tables(page_size, kv_lens, new_lens, free_pages, page_table, capacity, out)
     n, width = page_table.shape
@@ -466,7 +470,7 @@ def page_tables(page_size: int, kv_lens, new_lens, free_pages, page_table, capac
     status = lib.kascade_page_tables(
         n, page_size, width, _dense(kv_lens, i32, n, dev, where), _dense(new_lens, i32, n, dev, where),
         _dense(free_pages, i32, free, dev, where), free, _dense(page_table, i32, n * width, dev, where), lp, op, sp,
-        capacity, ip, _stream(None))
+        capacity, ip, raw)
     if status:
         raise KascadeError(status, where)
     return out
@@ -478,7 +482,8 @@ def q8_append(cache: Q8Cache, k, v, slot_map, ws=None, stream=None):
     slot_map [T]."""
     where = "kascade_q8_append"
     dev = cache.index
-    if dev < 0 or not _here(dev, stream):
+    raw = _here(dev, stream)
+    if raw is None:
         _need(dev >= 0, where)
         with _on(cache.device, stream, where):
             return q8_append(cache, k, v, slot_map, ws)
@@ -491,7 +496,7 @@ def q8_append(cache: Q8Cache, k, v, slot_map, ws=None, stream=None):
     _need(kd == 1 and vd == 1, where, ERR_UNSUPPORTED)
     p, n = ws.args() if ws is not None else (None, 0)
     status = lib.kascade_q8_append(cache.ref, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, _DTYPES[dtype], t,
-                                   _dense(slot_map, torch.int32, t, dev, where), p, n, _stream(None))
+                                   _dense(slot_map, torch.int32, t, dev, where), p, n, raw)
     if status:
         raise KascadeError(status, where)
 
@@ -504,7 +509,8 @@ def q8_gather(cache: Q8Cache, page_table, n_ctx: int, kv_lens=None, k=None, v=No
     where = "kascade_q8_gather"
     dev, i32 = cache.index, torch.int32
     _need(page_table.dim() == 2 and dev >= 0, where)
-    if not _here(dev, stream):
+    raw = _here(dev, stream)
+    if raw is None:
         with _on(cache.device, stream, where):
             return q8_gather(cache, page_table, n_ctx, kv_lens, k, v, dtype, ws)
     b, width = page_table.shape
@@ -520,7 +526,7 @@ def q8_gather(cache: Q8Cache, page_table, n_ctx: int, kv_lens=None, k=None, v=No
         cache.ref, b, n_ctx, _dense(page_table, i32, b * width, dev, where), width,
         None if kv_lens is None else _dense(kv_lens, i32, b, dev, where), _DTYPES[one],
         None if k is None else _dense(k, one, total, dev, where),
-        None if v is None else _dense(v, one, total, dev, where), p, n, _stream(None))
+        None if v is None else _dense(v, one, total, dev, where), p, n, raw)
     if status:
         raise KascadeError(status, where)
     return k, v
@@ -532,11 +538,12 @@ def sparse_decode_q8(shape: Shape, q, cache: Q8Cache, page_table, idx=None, head
     [B, Hq, 1, d] over an 8-bit paged cache, page_table [B, max_pages]."""
     where = "kascade_sparse_decode_q8"
     dev, i32 = cache.index, torch.int32
-    if dev < 0 or not _here(dev, stream):
+    raw = _here(dev, stream)
+    if raw is None:
         _need(dev >= 0, where)
         with _on(cache.device, stream, where):
             return sparse_decode_q8(shape, q, cache, page_table, idx, head_map, kv_lens, o, lse, ws)
-    b, hq = shape.batch, shape.num_q_heads
+    b, hq, lists = shape.batch, shape.num_q_heads, shape.n_lists
     n_q = b * hq * shape.head_dim
     dt = torch.float16 if shape.dtype == DTYPE_F16 else torch.bfloat16
     _need(page_table.dim() == 2, where)
@@ -547,13 +554,17 @@ def sparse_decode_q8(shape: Shape, q, cache: Q8Cache, page_table, idx=None, head
         op = o.data_ptr()
     else:
         op = _dense(o, dt, n_q, dev, where)
-    p, n = (Workspace(shape, (OP_SPARSE_DECODE_Q8,), device=cache.device) if ws is None else ws).args()
+    if ws is None:
+        ws = Workspace(shape, (OP_SPARSE_DECODE_Q8,), device=cache.device)
+    p, n = ws.args()
+    if idx is not None:   # B lists K entries, K = ceil(frac N)
+        count = -(-shape.topk_num * shape.kv_len // max(shape.topk_den, 1))
+        idx = _dense(idx, i32, b * lists * count, dev, where)
     status = lib.kascade_sparse_decode_q8(
         ctypes.byref(shape), cache.ref, qp, _dense(page_table, i32, b * width, dev, where), width,
-        None if kv_lens is None else _dense(kv_lens, i32, b, dev, where),
-        None if idx is None else _dense(idx, i32, index_count(shape), dev, where),
-        None if head_map is None else _dense(head_map, i32, shape.n_lists, dev, where), op,
-        None if lse is None else _dense(lse, torch.float32, b * hq, dev, where), p, n, _stream(None))
+        None if kv_lens is None else _dense(kv_lens, i32, b, dev, where), idx,
+        None if head_map is None else _dense(head_map, i32, lists, dev, where), op,
+        None if lse is None else _dense(lse, torch.float32, b * hq, dev, where), p, n, raw)
     if status:
         raise KascadeError(status, where)
     return o
