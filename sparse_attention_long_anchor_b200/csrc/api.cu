@@ -939,7 +939,7 @@ int kascade_sparse_decode_q8(const kascade_shape* s, const kascade_q8_cache* c, 
   a.num = t.num;
   a.den = t.den;
   a.stride = idx ? topk_count(t.N, t.num, t.den) : t.N;
-  a.den_inv = ~0ull / (uint32_t)t.den + 1;
+  a.den_inv = q8_reciprocal(t.den);
   a.n_lists = t.n_lists;
   a.max_pages = max_pages;
   a.one_list = t.one_list;

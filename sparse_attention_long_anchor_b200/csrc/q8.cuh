@@ -129,7 +129,7 @@ struct Q8DecodeArgs {
   int* err;
   int B, Hq, Hp, G, Gkv, N, num, den, n_lists, max_pages;
   int stride;                  // entries of a list (dense: N)
-  uint64_t den_inv;            // floor((2^64 - 1) / den) + 1
+  uint64_t den_inv;            // q8_reciprocal(den)
   bool one_list;
   int longest;                 // tiles of the longest list
   int ctas;                    // CTAs (not of clusters)

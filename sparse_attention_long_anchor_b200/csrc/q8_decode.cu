@@ -35,11 +35,13 @@
 //     `per` tiles each and push their partial results into one another's
 //     shared memory (st.async on the receiver's mbarrier; the one wait is
 //     bounded).  One launch, no workspace; latency is what counts there;
-//   * up to as many problems as CTAs are resident at once: all tiles are cut
-//     into shares, as many CTAs to a problem as its length asks for and all of
-//     them resident together (see find_share).  A ragged batch is balanced that
-//     way whatever its lengths are, which only the device knows;
-//   * more problems: `per` tiles to a CTA, in several waves.
+//   * longer lists, up to a quarter as many problems as CTAs are resident at
+//     once: all tiles are cut into shares, as many CTAs to a problem as its
+//     length asks for and all of them resident together (see find_share).  A
+//     ragged batch is balanced that way whatever its lengths are, which only
+//     the device knows;
+//   * more problems: `per` tiles to a CTA, in several waves.  A share would be
+//     most of a problem, and the longest would be waited for.
 // The last two leave a partial result (max, sum, fp32 output) per CTA in the
 // workspace where a problem has several, and a second kernel, launched to
 // overlap, joins them.  The split depends on the lengths alone and there are
@@ -139,12 +141,7 @@ __device__ __forceinline__ int row_keys(const Q8DecodeArgs& a, int b) {
   return a.kv_lens ? min(max(__ldg(a.kv_lens + b), 0), a.N) : a.N;
 }
 __device__ __forceinline__ int row_count(const Q8DecodeArgs& a, int n) {
-  if (!a.idx) return n;
-  // ceil(n num / den) by den's 64-bit reciprocal M = floor((2^64 - 1) / den) + 1:
-  // M exceeds 2^64 / den by at most 1, so the product is off by less than
-  // x / 2^64 <= 2^-23, which is less than 1 / den (x < 2^41, den <= 2^20)
-  const uint64_t x = (uint64_t)n * (uint32_t)a.num + (uint32_t)(a.den - 1);
-  return a.den == 1 ? (int)x : (int)__umul64hi(x, a.den_inv);
+  return a.idx ? q8_count(n, a.num, a.den, a.den_inv) : n;
 }
 __device__ __forceinline__ int row_tiles(const Q8DecodeArgs& a, int b) {
   return (row_count(a, row_keys(a, b)) + kTile - 1) / kTile;
@@ -741,7 +738,13 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(const Q8DecodeArg
 constexpr int kSizes[] = {16, 8, 4, 2};
 constexpr int kNumSizes = 4;
 constexpr int kClusterTiles = 16;  // most tiles of a warp in the first way
-constexpr int kWaveTiles = 64;     // tiles of a CTA in the third way
+// The second way up to this many problems, the third from there on: 128 problems
+// of 64K keys 342 against 322 us, 256 ragged ones up to 8K 77 against 58 us; 64
+// ragged ones up to 64K 104 against 112 us.
+constexpr int kShareProblems = kResident / 4;
+// Tiles of a CTA in the third way: 256 problems ragged up to 512 tiles 58 us by
+// 128 and 63 by 256, 128 problems of 4096 tiles 344 and 322 us.
+int wave_tiles(int longest) { return longest < 2048 ? 128 : 256; }
 
 template <int D, int QT, int CT>
 const int* active_clusters() {
@@ -800,7 +803,7 @@ cudaError_t run(Q8DecodeArgs a, cudaStream_t st) {
   const auto fn = q8_decode_kernel<D, QT, CT, false>;
   cudaError_t e = ensure_func_attrs(reinterpret_cast<const void*>(fn), Smem<D>::total, false);
   if (e != cudaSuccess) return e;
-  a.per = problems > kResident ? kWaveTiles : 0;
+  a.per = problems > kShareProblems ? wave_tiles(tiles) : 0;
   e = launch_ex(fn, dim3((unsigned)a.ctas), dim3(kThreads), Smem<D>::total, st, pdl, 1, a);
   if (e != cudaSuccess) return e;
   // the join waits for the kernel above before it reads anything, so it may always be launched early
@@ -820,8 +823,8 @@ Q8Plan q8_decode_plan(int64_t problems, int count) {
   if (p.longest <= kWarps) {
     p.ctas = problems;
     p.parts = 0;
-  } else if (problems > kResident) {
-    const int n = (p.longest + kWaveTiles - 1) / kWaveTiles;
+  } else if (problems > kShareProblems) {
+    const int n = (p.longest + wave_tiles(p.longest) - 1) / wave_tiles(p.longest);
     p.ctas = problems * n;
     p.parts = p.ctas;
   } else {

@@ -49,6 +49,22 @@ Q8_HD int q8_owner(const int* pre, int n, int x) {
   return lo;
 }
 
+// ceil(n num / den), 0 <= n, num, den <= 2^20, by den's 64-bit reciprocal
+// inv = floor((2^64 - 1) / den) + 1: inv exceeds 2^64 / den by at most 1, so the
+// product is off by less than x / 2^64 < 2^-23, which is less than 1 / den
+// (x < 2^41).  A 64-bit quotient would cost a kernel's first load hundreds of
+// cycles.
+Q8_HD uint64_t q8_reciprocal(uint32_t den) { return ~(uint64_t)0 / den + 1; }
+Q8_HD int32_t q8_count(int32_t n, uint32_t num, uint32_t den, uint64_t inv) {
+  const uint64_t x = (uint64_t)n * num + (den - 1);
+  if (den == 1) return (int32_t)x;
+#if defined(__CUDA_ARCH__)
+  return (int32_t)__umul64hi(x, inv);
+#else
+  return (int32_t)(((unsigned __int128)x * inv) >> 64);
+#endif
+}
+
 // Exponent of a block's scale: the smallest e with amax <= top 2^e, top =
 // 448 = 1.75 2^8 (e4m3) or 127 = 1.984375 2^6 (int8), from the bits of amax
 // (finite, >= 0), held in [-100, 122] so that 2^e and 2^-e are normal.

@@ -153,6 +153,47 @@ def test_append_long_prompt_takes_the_tiled_form(kind):
         _append_and_check(cache, kind, x[0].transpose(0, 1), x[1].transpose(0, 1), _slots(kv, new, rows, page))
 
 
+@pytest.mark.parametrize("kind,dtype,d,page,block", [
+    ("e4m3", torch.float32, 64, 64, 1), ("int8", torch.float16, 64, 16, 4), ("int8", torch.bfloat16, 128, 256, 256),
+    ("e4m3", torch.float16, 128, 64, 64), ("int8", torch.float32, 64, 128, 128), ("e4m3", torch.bfloat16, 64, 32, 2)])
+def test_append_tiled_form_values_gaps_and_old_rows(kind, dtype, d, page, block):
+    """Many heads bring few tokens to the form for prompts: skipped tokens
+    inside and between runs, infinities and NaN, zero rows, blocks whose scale
+    grows over their old rows, and a caller's scale that is no power of two."""
+    kc = _kc()
+    hkv = 32
+    kv, new = [block // 2, 3, 2 * page - 1], [520, 40, 333]
+    lens = [a + b + 2 for a, b in zip(kv, new)]
+    width = max(-(-n // page) for n in lens)
+    num = sum(-(-n // page) for n in lens) + 1
+    rows, _ = tables_for(lens, page, width, num, d + block)
+    cache = random_cache(kc, num, hkv, page, d, block, kind, block)
+    cache.scales[:, ::3] *= 0.7
+    g = torch.Generator().manual_seed(block)
+    slots = []
+    for i, sl in enumerate(_slots(kv, new, rows, page)):
+        slots.append(sl)
+        if i % 97 == 50:
+            slots += [-1] * (i % 31 + 1)
+        if i in (519, 559):
+            slots += [-1] * 90
+    t = len(slots)
+    x = torch.randn(t, 2, hkv, d, generator=g) * torch.exp2(torch.randint(-5, 6, (t, 2, hkv, 1), generator=g).float())
+    x[60:70] = 0.0
+    x[100, 0, ::2, 3] = float("inf")
+    x[101:103, 1, 1, 4] = float("-inf")
+    x[200, :, 5] = float("nan")
+    x[300:300 + block, :, 7, :] = float("nan")
+    x = x.to(dtype).cuda()
+    ws = kc.Workspace(kc.Shape.make(1, 2, 2, 64, 1, 16), (kc.OP_DENSE,))
+    _append_and_check(cache, kind, x[:, 0], x[:, 1], slots, ws)
+    assert ws.error() == 0
+    bad = list(slots)
+    bad[10], bad[400] = num * page, -7
+    _append_and_check(cache, kind, x[:, 1], x[:, 0], bad, ws)
+    assert ws.error(clear=True) == kc.DEVERR_PAGE
+
+
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
 def test_append_values_at_the_edges(kind):
     """Zero blocks, infinities, NaN, the largest and smallest magnitudes, values

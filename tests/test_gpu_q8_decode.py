@@ -121,7 +121,8 @@ def test_many_splits(n, lens, frac):
 
 
 @pytest.mark.parametrize("B,hkv,n,frac", [(40, 2, 600, None), (70, 1, 900, (40, 100)), (33, 8, 300, None),
-                                          (100, 3, 1400, None), (160, 2, 200, None), (148, 2, 260, None)])
+                                          (100, 3, 1400, None), (160, 2, 200, None), (148, 2, 260, None),
+                                          (38, 2, 2400, None), (37, 2, 3000, None), (74, 1, 4200, None)])
 def test_batches_past_a_warp_of_rows_and_past_the_resident_ctas(B, hkv, n, frac):
     """More rows than a warp counts at once; more problems than CTAs run at
     once, with one and several CTAs to a problem; as many as they are."""
@@ -190,18 +191,25 @@ def test_query_of_zeros_infinities_and_nan():
     assert torch.equal(o[:, keep], ref[:, keep]) and torch.isfinite(ref).all()
 
 
-def test_flags_give_the_same_bits():
+@pytest.mark.parametrize("B,n", [(1, 100), (1, 6000), (1, 40000), (50, 1500)])
+def test_flags_give_the_same_bits(B, n):
+    """A CTA to a list, clusters, shares and waves: calls launched to overlap
+    their predecessors, sharing one workspace and the outputs' memory."""
     kc = _kc()
-    cache = random_cache(kc, 100, 2, 64, 128, 64, "e4m3", 6)
-    t = _i([list(range(100))])
-    for n in (100, 6000):
-        s = kc.Shape.make(1, 8, 2, 128, 1, n)
-        q = torch.randn(1, 8, 1, 128, generator=torch.Generator().manual_seed(n)).bfloat16().cuda()
-        ws = kc.Workspace(s, (kc.OP_SPARSE_DECODE_Q8,))
-        ref = kc.sparse_decode_q8(s, q, cache, t, ws=ws)
+    per = -(-n // 64)
+    cache = random_cache(kc, 700, 2, 64, 128, 64, "e4m3", 6)
+    t = _i([[(b * 13 + i) % 700 for i in range(per)] for b in range(B)])
+    s = kc.Shape.make(B, 8, 2, 128, 1, n)
+    qs = [torch.randn(B, 8, 1, 128, generator=torch.Generator().manual_seed(n + i)).bfloat16().cuda() for i in range(2)]
+    lens = _i([max(1, n - 31 * b) for b in range(B)])
+    ws = kc.Workspace(s, (kc.OP_SPARSE_DECODE_Q8,))
+    for kv in (None, lens):
+        ref = [kc.sparse_decode_q8(s, q, cache, t, kv_lens=kv, ws=ws).clone() for q in qs]
         for flags in (kc.FLAG_PDL, kc.FLAG_PDL | kc.FLAG_INPUTS_STABLE):
-            outs = [kc.sparse_decode_q8(s.with_flags(flags), q, cache, t, ws=ws) for _ in range(20)]
-            assert all(torch.equal(o, ref) for o in outs)
+            outs = [kc.sparse_decode_q8(s.with_flags(flags), qs[i % 2], cache, t, kv_lens=kv, ws=ws) for i in range(20)]
+            torch.cuda.synchronize()
+            assert ws.error() == 0
+            assert all(torch.equal(o, ref[i % 2]) for i, o in enumerate(outs))
 
 
 def test_bad_list_and_table_entries_are_reported():

@@ -78,6 +78,26 @@ def test_owner_skips_empty_requests(tmp_path):
     assert list(map(int, _run(tmp_path, "\n".join(body)))) == want
 
 
+def test_list_lengths_by_reciprocal(tmp_path):
+    """ceil(n num / den) at and around every kind of border, up to the largest
+    lengths and budgets that a call takes."""
+    top = 1 << 20
+    rng = np.random.default_rng(0)
+    cases = [(n, num, den) for den in (1, 2, 3, 7, 10, 100, 255, 256, 4099, 99991, top - 1, top)
+             for num in {1, den, max(1, den // 3), max(1, den - 1)} for n in (0, 1, 2, den - 1, den, min(den + 1, top), 3277, 65535, top - 1, top)]
+    for _ in range(3000):
+        den = int(rng.integers(1, top + 1))
+        num = int(rng.integers(1, den + 1))
+        n = int(rng.integers(0, top + 1))
+        k = int(rng.integers(0, top * num // den + 1))          # n num a multiple of den, or next to one
+        cases += [(n, num, den), (min(top, k * den // num), num, den), (min(top, k * den // num + 1), num, den)]
+    cases = [c for c in cases if c[1] <= c[2] <= top and c[0] <= top]
+    body = ["static const int c[][3] = {%s};" % ", ".join("{%d,%d,%d}" % c for c in cases),
+            'for (auto& x : c) std::printf("%d\\n", q8_count(x[0], x[1], x[2], q8_reciprocal(x[2])));']
+    got = list(map(int, _run(tmp_path, "\n".join(body))))
+    assert got == [-(-n * num // den) for n, num, den in cases]
+
+
 def test_scale_exponents(tmp_path):
     vals = [0.0, 1.0, 448.0, 448.0 * (1 + 2 ** -20), 447.9, 127.0, 127.0 * (1 + 2 ** -20), 126.9, 3e38, 1e-44, 2.0 ** -95,
             2.0 ** -130, 1e30, 0.3]
