@@ -452,7 +452,9 @@ KASCADE_API int kascade_q8_gather(const kascade_q8_cache* cache, int32_t batch, 
  *            list does (the call says KASCADE_ERR_WORKSPACE otherwise)
  * q, o: shape->dtype bf16 or fp16 (KASCADE_ERR_UNSUPPORTED for fp32).  Range
  * checks are always on; KASCADE_FLAG_CHECK_INDICES is refused.  With
- * KASCADE_FLAG_INPUTS_STABLE the call still waits before it reads.
+ * KASCADE_FLAG_INPUTS_STABLE, the cache's pages and scales, page_table and
+ * kv_lens count among the inputs that must be two launches old (not so right
+ * after the kascade_q8_append of the same layer).
  * The V scales of the keys that one row attends over should lie within a
  * factor of 2^24 of one another: values of blocks below that keep fewer bits.
  */

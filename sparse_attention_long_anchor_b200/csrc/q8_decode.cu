@@ -136,9 +136,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // weight of a partial result with running maximum m when joined at M
 __device__ __forceinline__ float join_weight(float m, float M) { return m == -INFINITY ? 0.0f : ex2_fast(m - M); }
 
+// (Inputs are read by plain loads, not through the read-only path: under
+// programmatic dependent launch another kernel may write them while this one
+// is already running, up to its wait.)
 // keys that batch row b's problems attend over, and their tiles
 __device__ __forceinline__ int row_keys(const Q8DecodeArgs& a, int b) {
-  return a.kv_lens ? min(max(__ldg(a.kv_lens + b), 0), a.N) : a.N;
+  return a.kv_lens ? min(max(a.kv_lens[b], 0), a.N) : a.N;
 }
 __device__ __forceinline__ int row_count(const Q8DecodeArgs& a, int n) {
   return a.idx ? q8_count(n, a.num, a.den, a.den_inv) : n;
@@ -256,8 +259,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
   extern __shared__ __align__(128) char smem[];
   float2* red_ml = reinterpret_cast<float2*>(smem + L::ml);
   float* red_e = reinterpret_cast<float*>(smem + L::e);
-  pdl_wait();
-  pdl_launch_dependents();
+  // with inputs that the caller vouches for, everything up to the copies of
+  // the first tiles comes before the wait for the previous kernel; what that
+  // may have written (q) or still reads (the workspace, o) comes behind it
+  const bool early = (a.flags & 3) == 3;
+  if (!early) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int G = a.G;
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
 
   // the head map's entries, a lane each: they do not wait for (b, h)
   const bool mapped = a.idx && a.head_map && !a.one_list;
-  const int hm_lane = mapped && lane < a.Hp ? __ldg(a.head_map + lane) : 0;
+  const int hm_lane = mapped && lane < a.Hp ? a.head_map[lane] : 0;
   const int stride = a.stride;   // entries of a list, -1 past a row's own (dense: N)
   // this CTA's tiles, from tile ta of problem (b, h) on
   int b, h, ta, per = a.per;
@@ -302,8 +311,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
     } else {
       const int mine = first_rows(a);
       per = find_share(a, mine);
-      if (blockIdx.x == 0 && tid == 0) *a.share = per;   // for the join
-      if (!part_of_cta(a, mine, per, blockIdx.x, pt)) return;
+      if (blockIdx.x == 0) {   // for the join
+        if (early) pdl_wait();
+        if (tid == 0) *a.share = per;
+      }
+      if (!part_of_cta(a, mine, per, blockIdx.x, pt)) {
+        if (early) pdl_wait();   // (no kernel of ours is done before its predecessor)
+        return;
+      }
     }
     b = pt.b;
     h = pt.h;
@@ -313,21 +328,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
   // Loads that wait for nothing but (b, h) come first: each is a trip of its
   // own to L2 or HBM.  q's rows: the dims of the lane's K chunks for head g.
   uint4 qw[KQ][2];
+  auto load_q = [&]() {
 #pragma unroll
-  for (int s = 0; s < KQ; ++s) {
-    qw[s][0] = qw[s][1] = make_uint4(0, 0, 0, 0);
-    if (g < G) {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                      ((size_t)b * a.Hq + h * G + g) * D + 16 * (KQ * c + s));
-      qw[s][0] = __ldg(p);
-      qw[s][1] = __ldg(p + 1);
+    for (int s = 0; s < KQ; ++s) {
+      qw[s][0] = qw[s][1] = make_uint4(0, 0, 0, 0);
+      if (g < G) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                        ((size_t)b * a.Hq + h * G + g) * D + 16 * (KQ * c + s));
+        qw[s][0] = p[0];
+        qw[s][1] = p[1];
+      }
     }
-  }
+  };
+  if (!early) load_q();
   const int n_b = row_keys(a, b);
   // the problem's keys: an index list (of another head's problem, by the
   // map; an entry out of range is an empty list) or all keys of the row
   int hm = a.one_list ? 0 : h;
-  if (mapped) hm = h < 32 ? __shfl_sync(0xffffffffu, hm_lane, h) : __ldg(a.head_map + h);
+  if (mapped) hm = h < 32 ? __shfl_sync(0xffffffffu, hm_lane, h) : a.head_map[h];
   const bool hm_ok = hm >= 0 && (a.idx == nullptr || hm < a.n_lists);
   const int32_t* list = a.idx ? a.idx + ((size_t)b * a.n_lists + (hm_ok ? hm : 0)) * stride : nullptr;
   const int kvh = (h * G) / a.Gkv;
@@ -341,13 +359,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
   auto place = [&](int pair) -> int { return (t0 + (2 * pair + (lane >> 4)) * kWarps) * kTile + (lane & 15); };
   auto entry = [&](int pair) -> int {
     const int k = min(place(pair), stride - 1);
-    return list ? __ldg(list + k) : k;
+    return list ? list[k] : k;
   };
   int e0 = entry(0), e1 = entry(1), e_n = entry(2);   // (e_n: of the pair whose pages are looked up next)
 
   const int count_b = row_count(a, n_b);
   const int tiles_b = (count_b + kTile - 1) / kTile;
-  if (!kCluster && ta >= tiles_b) return;   // (a row without keys is the join's)
+  if (!kCluster && ta >= tiles_b) {   // (a row without keys is the join's)
+    if (early) pdl_wait();
+    return;
+  }
   const int tb = min(tiles_b, ta + per);    // tiles [ta, tb) of the problem
   const int t_end = hm_ok ? tb : ta;
   auto key_of = [&](int pair, int e) -> int {   // -1: none
@@ -357,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
     if (bad) raise_error(a.err, kErrIndexRange);
     return key;
   };
-  auto page_of = [&](int key) -> int { return key < 0 ? 0 : __ldg(ptab + (key >> ps)); };
+  auto page_of = [&](int key) -> int { return key < 0 ? 0 : ptab[key >> ps]; };
   auto row_of = [&](int key, int page) -> uint32_t {
     if (key < 0) return kNoRow;
     bool bad = false;
@@ -407,6 +428,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
     cp_async_commit();
   }
 
+  if (early) {
+    pdl_wait();
+    pdl_launch_dependents();
+    load_q();
+  }
   // q as B operand of S^T, scaled into fp16
   uint32_t qf[KQ][4][2];
   float sc0, sc1;   // score scale of heads 2c and 2c + 1: log2(e) / sqrt(D) and q's power of two

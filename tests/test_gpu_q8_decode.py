@@ -210,6 +210,15 @@ def test_flags_give_the_same_bits(B, n):
             torch.cuda.synchronize()
             assert ws.error() == 0
             assert all(torch.equal(o, ref[i % 2]) for i, o in enumerate(outs))
+        # each call's query is the output of the call before it
+        chains = []
+        for flags in (0, kc.FLAG_PDL, kc.FLAG_PDL | kc.FLAG_INPUTS_STABLE):
+            x = [qs[0].clone(), torch.empty_like(qs[0])]
+            for i in range(24):
+                kc.sparse_decode_q8(s.with_flags(flags), x[i % 2], cache, t, kv_lens=kv, o=x[1 - i % 2], ws=ws)
+            torch.cuda.synchronize()
+            chains.append(x)
+        assert all(torch.equal(a, b) for c in chains[1:] for a, b in zip(c, chains[0]))
 
 
 def test_bad_list_and_table_entries_are_reported():
