@@ -83,8 +83,19 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int ch) {
   return (uint32_t)((r >> 1) * 128 + ((((r & 1) * 4 + ch) ^ (2 * ((r >> 1) & 3))) << 4));
 }
 
-// shared memory: the rings [kWarps][kStages]; after a problem's tiles each warp's ring holds its
-// output for the join of the warps
+// From the place of a chunk in row r to that of the same chunk in row r + 1 (r
+// even), and in row r + n (n a multiple of 4; D = 64: of 8).
+template <int D>
+__device__ __forceinline__ uint32_t next_row(uint32_t at) {
+  return D == 128 ? (at + 128) ^ 16 : at ^ 64;
+}
+template <int D>
+__device__ __forceinline__ uint32_t row_step(uint32_t at, int n) {
+  return D == 128 && (n & 4) ? ((at + n * D) ^ 64) : at + n * D;
+}
+
+// shared memory: the rings [kWarps][kStages]; after the tiles each warp's ring
+// holds its output for the join of the warps
 template <int D>
 struct Smem {
   static constexpr int RO = D + 4;             // padded row of a warp's output (floats)
@@ -356,12 +367,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
   // page-table entries, those ahead of the rows' copies.  Keys past the list
   // have no row: zeros are filled in for them and their scores masked.
   const int t0 = ta + warp;   // this warp's tiles: t0, t0 + kWarps, ...
-  auto place = [&](int pair) -> int { return (t0 + (2 * pair + (lane >> 4)) * kWarps) * kTile + (lane & 15); };
-  auto entry = [&](int pair) -> int {
-    const int k = min(place(pair), stride - 1);
+  constexpr int kPairStep = 2 * kWarps * kTile;   // from a pair's keys to the next pair's
+  const int place = (t0 + (lane >> 4) * kWarps) * kTile + (lane & 15);   // the lane's key of pair 0, in the list
+  auto entry = [&](int k) -> int {
+    k = min(k, stride - 1);
     return list ? list[k] : k;
   };
-  int e0 = entry(0), e1 = entry(1), e_n = entry(2);   // (e_n: of the pair whose pages are looked up next)
+  // list entries of the first pairs; e_n is that of the pair whose pages are looked up next
+  const int e0 = entry(place), e1 = entry(place + kPairStep);
+  int e_n = entry(place + 2 * kPairStep), k_n = place + 2 * kPairStep;
 
   const int count_b = row_count(a, n_b);
   const int tiles_b = (count_b + kTile - 1) / kTile;
@@ -371,60 +385,63 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
   }
   const int tb = min(tiles_b, ta + per);    // tiles [ta, tb) of the problem
   const int t_end = hm_ok ? tb : ta;
-  auto key_of = [&](int pair, int e) -> int {   // -1: none
-    if (place(pair) >= count_b) return -1;
+  // Entries out of range are replaced and noted; reported once, at the end.
+  bool bad_key = false, bad_page = false;
+  auto key_of = [&](int k, int e) -> int {
     bool bad = false;
     const int key = q8_key(e, n_b, bad);
-    if (bad) raise_error(a.err, kErrIndexRange);
+    bad_key |= bad && k < count_b;
     return key;
   };
-  auto page_of = [&](int key) -> int { return key < 0 ? 0 : ptab[key >> ps]; };
-  auto row_of = [&](int key, int page) -> uint32_t {
-    if (key < 0) return kNoRow;
+  auto row_of = [&](int k, int key, int page) -> uint32_t {
     bool bad = false;
     const uint32_t pg = q8_page(page, a.c.num_pages, bad);
-    if (bad) raise_error(a.err, kErrPage);
-    return q8_row(pg, (uint32_t)key & ((1u << ps) - 1u), kvh, a.c.Hkv, ps);
+    bad_page |= bad && k < count_b;
+    const uint32_t row = q8_row(pg, (uint32_t)key & ((1u << ps) - 1u), kvh, a.c.Hkv, ps);
+    return k < count_b ? row : kNoRow;
   };
-  // copies of tile t (the second of its pair: `odd`) into a slot of the ring
-  auto issue = [&](uint32_t mine, int t, int odd, int slot) {
-    const uint32_t st = ring + (uint32_t)(slot * St::BYTES);
-    if ((t + 1) * kTile <= count_b) {
+  // copies of a tile (the second of its pair: `odd`) into a stage of the ring
+  const int whole_tiles = count_b / kTile;   // tiles without a masked tail
+  const uint32_t copy0 = chunk_at<D>(lane / LPR, lane % LPR);
+  const uint32_t copy_s = St::S + (lane & 15) * 8;
+  auto issue = [&](uint32_t mine, int t, int odd, uint32_t st) {
+    const int r0 = lane / LPR + 16 * odd;
+    if (t < whole_tiles) {
 #pragma unroll
       for (int i = 0; i < 16 / RPC; ++i) {
-        const int r = lane / LPR + i * RPC, ch = lane % LPR;
-        const uint32_t row = __shfl_sync(0xffffffffu, mine, r + 16 * odd);
-        cp_async_16(st + St::K + chunk_at<D>(r, ch), kp + (size_t)row * D, 16);
-        cp_async_16(st + St::V + chunk_at<D>(r, ch), vp + (size_t)row * D, 16);
+        const uint32_t row = __shfl_sync(0xffffffffu, mine, r0 + i * RPC);
+        const uint32_t to = st + row_step<D>(copy0, i * RPC);
+        cp_async_16(to + St::K, kp + (size_t)row * D, 16);
+        cp_async_16(to + St::V, vp + (size_t)row * D, 16);
       }
-      if ((lane >> 4) == odd) cp_async_8(st + St::S + (lane & 15) * 8, a.c.scales + (mine >> bs), 8);
+      if ((lane >> 4) == odd) cp_async_8(st + copy_s, a.c.scales + (mine >> bs), 8);
     } else {
 #pragma unroll 1
       for (int i = 0; i < 16 / RPC; ++i) {
-        const int r = lane / LPR + i * RPC, ch = lane % LPR;
-        const uint32_t row = __shfl_sync(0xffffffffu, mine, r + 16 * odd);
+        const uint32_t row = __shfl_sync(0xffffffffu, mine, r0 + i * RPC);
         const int bytes = row == kNoRow ? 0 : 16;   // 0: zeros, and nothing is read
         const size_t off = row == kNoRow ? 0 : (size_t)row * D;
-        cp_async_16(st + St::K + chunk_at<D>(r, ch), kp + off, bytes);
-        cp_async_16(st + St::V + chunk_at<D>(r, ch), vp + off, bytes);
+        const uint32_t to = st + chunk_at<D>(lane / LPR + i * RPC, lane % LPR);
+        cp_async_16(to + St::K, kp + off, bytes);
+        cp_async_16(to + St::V, vp + off, bytes);
       }
       if ((lane >> 4) == odd)
-        cp_async_8(st + St::S + (lane & 15) * 8, a.c.scales + (mine == kNoRow ? 0u : mine >> bs), mine == kNoRow ? 0 : 8);
+        cp_async_8(st + copy_s, a.c.scales + (mine == kNoRow ? 0u : mine >> bs), mine == kNoRow ? 0 : 8);
     }
   };
   // the first kStages tiles on their way
   static_assert(kStages == 3, "two pairs cover the tiles issued up front and the next one");
   uint32_t rows = kNoRow, rows_n = kNoRow;   // rows of the pair that is issued from, and of the next one
   if (t0 < t_end) {
-    const int k0 = key_of(0, e0), k1 = key_of(1, e1);
-    const int p0 = page_of(k0), p1 = page_of(k1);
-    const uint32_t r0 = row_of(k0, p0);
-    rows = row_of(k1, p1);
-    issue(r0, t0, 0, 0);
+    const int k0 = key_of(place, e0), k1 = key_of(place + kPairStep, e1);
+    const int p0 = ptab[k0 >> ps], p1 = ptab[k1 >> ps];
+    const uint32_t r0 = row_of(place, k0, p0);
+    rows = row_of(place + kPairStep, k1, p1);
+    issue(r0, t0, 0, ring);
     cp_async_commit();   // one group per stage, empty past the last tile
-    if (t0 + kWarps < t_end) issue(r0, t0 + kWarps, 1, 1);
+    if (t0 + kWarps < t_end) issue(r0, t0 + kWarps, 1, ring + St::BYTES);
     cp_async_commit();
-    if (t0 + 2 * kWarps < t_end) issue(rows, t0 + 2 * kWarps, 0, 2);
+    if (t0 + 2 * kWarps < t_end) issue(rows, t0 + 2 * kWarps, 0, ring + 2 * St::BYTES);
     cp_async_commit();
   }
 
@@ -480,27 +497,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
 #pragma unroll
   for (int t = 0; t < MT; ++t) oacc[t][0] = oacc[t][1] = oacc[t][2] = oacc[t][3] = 0.f;
 
-  int slot = 0, it = 0;
+  // this lane's chunks in a stage: K rows g and g + 8, V rows 2c, 2c + 1, + 8
+  const uint32_t k_at = St::K + chunk_at<D>(g, KQ * c);
+  const uint32_t v_at = St::V + (D == 128 ? chunk_at<D>(2 * c, g) : chunk_at<D>(2 * c, g >> 1) + (g & 1) * 8);
+  uint32_t st = ring;
+  int it = 0;
 #pragma unroll 1
   for (int t = t0; t < t_end; t += kWarps, ++it) {
     // tile it + kStages is issued below: the first of pair (it + 3) / 2 when
     // `it` is odd, and then the next pair's rows have been found
     const bool find = !(it & 1) && t + (kStages + 1) * kWarps < t_end;
-    int k2 = -1, pg2 = 0;
+    int key2 = 0, page2 = 0;
     if (find) {
-      k2 = key_of((it + 4) >> 1, e_n);
-      pg2 = page_of(k2);
-      e_n = entry((it + 6) >> 1);
+      key2 = key_of(k_n, e_n);
+      page2 = ptab[key2 >> ps];
+      e_n = entry(k_n + kPairStep);
     }
     cp_async_wait<kStages - 1>();   // this lane's copies of the tile
     __syncwarp();                   // ... and every other lane's
-    const uint32_t st = ring + (uint32_t)(slot * St::BYTES);
     const uint2 s0 = lds_v2(st + St::S + g * 8), s1 = lds_v2(st + St::S + (g + 8) * 8);
     float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < KQ; ++s) {
-      const uint4 ka = lds_v4(st + St::K + chunk_at<D>(g, KQ * c + s));
-      const uint4 kb = lds_v4(st + St::K + chunk_at<D>(g + 8, KQ * c + s));
+      const uint32_t at = st + (k_at ^ (16u * s));   // (KQ c is even: the next chunk's place is the other of a pair)
+      const uint4 ka = lds_v4(at), kb = lds_v4(at + 8 * D);
       const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -555,12 +575,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
     uint32_t v[4][VW];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = 2 * c + (j & 1) + 4 * (j & 2);
+      const uint32_t at = st + (j & 1 ? next_row<D>(v_at) : v_at) + (j >> 1) * 8 * D;
       if constexpr (D == 128) {
-        const uint4 x = lds_v4(st + St::V + chunk_at<D>(r, g));
+        const uint4 x = lds_v4(at);
         v[j][0] = x.x, v[j][1] = x.y, v[j][VW - 2] = x.z, v[j][VW - 1] = x.w;
       } else {
-        const uint2 x = lds_v2(st + St::V + chunk_at<D>(r, g >> 1) + (g & 1) * 8);
+        const uint2 x = lds_v2(at);
         v[j][0] = x.x, v[j][1] = x.y;
       }
     }
@@ -575,11 +595,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
     }
     __syncwarp();   // every lane has read the stage
     if (it & 1) rows = rows_n;
-    if (t + kStages * kWarps < t_end) issue(rows, t + kStages * kWarps, (it + kStages) & 1, slot);
+    if (t + kStages * kWarps < t_end) issue(rows, t + kStages * kWarps, (it + kStages) & 1, st);
     cp_async_commit();
-    if (find) rows_n = row_of(k2, pg2);
-    slot = slot + 1 == kStages ? 0 : slot + 1;
+    if (find) {
+      rows_n = row_of(k_n, key2, page2);
+      k_n += kPairStep;
+    }
+    st = st + St::BYTES == ring + kStages * St::BYTES ? ring : st + St::BYTES;
   }
+  if (bad_key) raise_error(a.err, kErrIndexRange);
+  if (bad_page) raise_error(a.err, kErrPage);
   cp_async_wait<0>();
   __syncwarp();
 
