@@ -46,6 +46,8 @@
 // workspace where a problem has several, and a second kernel, launched to
 // overlap, joins them.  The split depends on the lengths alone and there are
 // no atomics: results do not depend on the order in which CTAs run.
+#include <atomic>
+
 #include "cluster_choice.h"
 #include "kernels.h"
 #include "q8.cuh"
@@ -808,11 +810,14 @@ int wave_tiles(int longest) { return longest < 2048 ? 128 : 256; }
 
 template <int D, int QT, int CT>
 const int* active_clusters() {
-  static int cached[64][kNumSizes + 1] = {{0}};   // [0]: 1 once filled
+  // (host threads may come here at once: each fills the same numbers in, and
+  // `ready` is set behind them)
+  static int cached[64][kNumSizes];
+  static std::atomic<bool> ready[64];
   static const int none[kNumSizes] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return none;
-  if (!cached[dev][0]) {
+  if (!ready[dev].load(std::memory_order_acquire)) {
     for (int i = 0; i < kNumSizes; ++i) {
       int m = 0;
       const auto fn = q8_decode_kernel<D, QT, CT, true>;
@@ -830,12 +835,12 @@ const int* active_clusters() {
         cfg.numAttrs = 1;
         if (cudaOccupancyMaxActiveClusters(&m, fn, &cfg) != cudaSuccess) m = 0;
       }
-      cached[dev][1 + i] = m;
+      cached[dev][i] = m;
     }
     cudaGetLastError();
-    cached[dev][0] = 1;
+    ready[dev].store(true, std::memory_order_release);
   }
-  return &cached[dev][1];
+  return cached[dev];
 }
 
 template <int D, int QT, int CT>

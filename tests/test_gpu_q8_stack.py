@@ -173,6 +173,7 @@ def test_streams_and_two_calls_at_once():
             outs.append(kc.sparse_decode_q8(s, q, cache, t, stream=st))
             outs.append(kc.sparse_decode_q8(s, q, cache, t, stream=st.cuda_stream))
         outs.append(kc.sparse_decode_q8(s, q, cache, t))
+        outs.append(kc.sparse_decode_q8(s, q, cache, t, stream=0))
     k, v = kc.q8_gather(cache, t, 12000, _i([11111]), stream=streams[0])
     torch.cuda.synchronize()
     assert all(torch.equal(o, ref) for o in outs)
@@ -195,3 +196,69 @@ def test_streams_and_two_calls_at_once():
                              Q.rows_of(hv[1], hv[2], 1, [2, 3], 0, 100))
     # (bf16's half step of values up to 4, and the weights' fp16 rounding)
     assert np.abs(o[0, :4, 0].double().cpu().numpy() - want).max() <= 4 * 2.0 ** -8
+
+
+def test_calls_from_two_host_threads():
+    """The library is entered from several threads at once (the binding's calls
+    release the interpreter lock), on streams and workspaces of their own."""
+    import threading
+    kc = _kc()
+    from q8_cases import random_cache
+    cache = random_cache(kc, 200, 2, 64, 128, 64, "e4m3", 6)
+    t = _i([list(range(200))])
+    shapes = [kc.Shape.make(1, 8, 2, 128, 1, n) for n in (100, 3000, 12000)]
+    q = torch.randn(1, 8, 1, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    refs = [kc.sparse_decode_q8(s, q, cache, t) for s in shapes]
+    torch.cuda.synchronize()
+    got, bad = [], []
+
+    def work():
+        try:
+            st = torch.cuda.Stream()
+            for _ in range(20):
+                for s, ref in zip(shapes, refs):
+                    got.append((kc.sparse_decode_q8(s, q, cache, t, stream=st), ref))
+            st.synchronize()
+        except Exception as exc:   # noqa: BLE001  (reported below, from the test's own thread)
+            bad.append(exc)
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not bad, bad
+    assert len(got) == 240 and all(torch.equal(o, ref) for o, ref in got)
+
+
+def test_a_first_call_inside_a_capture():
+    """A process whose first call of each kind is captured."""
+    import subprocess
+    import sys
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch
+from sparse_attention_long_anchor_b200 import kascade as kc
+i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+c = kc.Q8Cache.empty(40, 2, 128, 64)
+kv, new, free, table = i([0]), i([2000]), i(list(range(40))), i([[-1] * 40])
+x = torch.randn(2000, 2, 128, device="cuda").bfloat16()
+s = kc.Shape.make(1, 8, 2, 128, 1, 2560)
+q = torch.randn(1, 8, 1, 128, device="cuda").bfloat16()
+ws = kc.Workspace(s, (kc.OP_SPARSE_DECODE_Q8,))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    lens, _, slots, info = kc.page_tables(64, kv, new, free, table, 2000)
+    kc.q8_append(c, x, x, slots)
+    o = kc.sparse_decode_q8(s, q, c, table, kv_lens=lens, ws=ws)
+    k, v = kc.q8_gather(c, table, 2560, lens)
+g.replay()
+torch.cuda.synchronize()
+want = kc.sparse_decode_q8(s, q, c, table, kv_lens=i([2000]))
+assert info.tolist() == [32, 2000] and torch.equal(o, want) and (o != 0).any() and ws.error() == 0
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
