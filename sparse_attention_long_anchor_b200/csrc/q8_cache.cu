@@ -152,9 +152,9 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const PageTabl
 // fifth of the second reads miss L2).  A decode step is bound by latency: 2.2
 // us for 8 requests.
 //
-// Two kernels, by the number of tokens (see run_append).  In both, a tile of
-// tokens owns the runs that start in it, and the heads of a token are worked on
-// next to one another: together they read whole stretches of memory.
+// Three kernels, by the block's size and the number of tokens (see run_append).
+// The heads of a token are worked on next to one another: together they read
+// whole stretches of memory.
 constexpr int kAppThreads = 256;
 constexpr int kAppWarps = kAppThreads / 32;
 constexpr int kShortRun = 8;   // rows of a run that a warp does alone
@@ -336,6 +336,10 @@ struct Appender {
   }
   __device__ __forceinline__ float* scale_at(uint32_t row) const { return scales + 2 * (size_t)(row >> a.c.block_shift); }
   __device__ __forceinline__ Raw8<IN> load(int t) const { return load8<IN>(src, (int64_t)t * ts + off); }
+  __device__ __forceinline__ const char* address(int t) const {
+    return static_cast<const char*>(src) + ((int64_t)t * ts + off) * (IN == kInF32 ? 4 : 2);
+  }
+  __device__ __forceinline__ int64_t token_bytes() const { return ts * (IN == kInF32 ? 4 : 2); }
   __device__ __forceinline__ void store_row(uint32_t row, const Raw8<IN>& r, float s) const {
     *reinterpret_cast<uint2*>(pages + (size_t)row * D + col) = pack8<IN, CT>(r, s);
   }
@@ -374,6 +378,52 @@ struct Appender {
     }
   }
 };
+
+// One scale per row (S = 1): rows have nothing to do with one another.  The lanes
+// of a row read it, find its maximum and scale, and write it, from registers;
+// kRowBatch rows per lane under way together.
+constexpr int kRowBatch = 4;
+template <int D, int IN, int CT>
+__global__ void __launch_bounds__(kAppThreads) q8_append_rows_kernel(const Q8AppendArgs a) {
+  using A = Appender<D, IN, CT>;
+  constexpr int GROUPS = kAppThreads / A::LPR;
+  const int sets = 2 * a.c.Hkv, total = a.T * sets;   // (31 bits: checked on the host)
+  const int u0 = blockIdx.x * (GROUPS * kRowBatch) + (int)threadIdx.x / A::LPR;
+  const int lane = threadIdx.x & 31;
+  const uint32_t row_lanes = ((1u << A::LPR) - 1u) << (lane / A::LPR * A::LPR);
+  Raw8<IN> v[kRowBatch];
+  int slot[kRowBatch];
+#pragma unroll
+  for (int i = 0; i < kRowBatch; ++i) {   // neighbouring lanes: the heads of a token
+    const int u = u0 + i * GROUPS;
+    slot[i] = -1;
+    if (u < total) {
+      const A ap(a, u % sets);
+      slot[i] = __ldg(a.slots + u / sets);
+      v[i] = ap.load(u / sets);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRowBatch; ++i) {
+    const int u = u0 + i * GROUPS;
+    const A ap(a, u % sets);
+    if (!ap.valid(slot[i])) {   // (the lanes of a row agree)
+      if (slot[i] != -1) raise_error(a.err, kErrPage);
+      continue;
+    }
+    MaxAcc<IN> acc;
+    acc.add(v[i]);
+    if (__any_sync(row_lanes, !acc.finite())) {
+      acc.m = 0;
+      acc.add_finite(v[i]);
+    }
+    const uint32_t row = ap.row_of(slot[i]);
+    float ratio;
+    const float s = ap.new_scale(__reduce_max_sync(row_lanes, acc.bits()), 0, 0.0f, ratio);
+    if (lane % A::LPR == 0) *ap.scale_at(row) = s;
+    *reinterpret_cast<uint2*>(ap.pages + (size_t)row * D + ap.col) = pack8_pow2<IN, CT>(v[i], 1.0f / s);
+  }
+}
 
 // Few tokens (a decode step): a token to a warp, which looks around it.  Runs of
 // up to kShortRun rows are the warp's, kept in registers; longer ones the CTA's.
@@ -461,167 +511,284 @@ __global__ void __launch_bounds__(kAppThreads) q8_append_kernel(const Q8AppendAr
   }
 }
 
-// Many tokens (prompts): a warp takes a tile's runs of one (kv head, tensor),
-// all at once whatever their lengths are; the CTA's warps take neighbouring
-// heads of the same tile, whose runs they find together, a token per thread.
-// Every row from the first start to the end of the last run is read and its
-// maximum joined to its run's (an integer maximum: order does not matter); a
-// lane per run finds its scale; then the rows are read again, from L1 or L2,
-// rounded and written.  What a row needs beside its values is found once per
-// CTA and kept in shared memory: instructions per value bound this kernel as
-// much as its bytes.
+// Many tokens (prompts): one, two or four warps take a tile's runs of one (kv
+// head, tensor), all at once whatever their lengths are; the CTA's warps take
+// neighbouring heads of the same tile, whose runs they find together, a token
+// per thread.  Every row from the first start to the end of the last run is
+// read into shared memory, where it waits for its run's scale: the maxima are
+// joined per run (integer maxima: order does not matter), a lane per run finds
+// the scale, then the rows are rounded and written.  (Windows that do not fit,
+// as at a border of two long runs, are read twice instead.)  What a row needs
+// beside its values is found once per CTA: instructions per value bound this
+// kernel as much as its bytes.
+constexpr int kTileWarps = 4;
+constexpr int kTileThreads = kTileWarps * 32;
+constexpr int kKept = 16384;   // bytes of shared memory per warp: three CTAs, 192 KB under way per SM
+
 template <int D, int IN, int CT>
-__global__ void __launch_bounds__(kAppThreads, 4) q8_append_tiled_kernel(const Q8AppendArgs a, int tile, int groups) {
+__global__ void __launch_bounds__(kTileThreads, 5)
+    q8_append_tiled_kernel(const Q8AppendArgs a, int tile, int groups, int wps, int hold) {
   using A = Appender<D, IN, CT>;
-  constexpr int kWindow = 2 * kMaxTile;          // rows looked at: a tile, and a block behind it
-  constexpr int BATCH = IN == kInF32 ? 4 : 8;    // loads of a lane under way together
-  __shared__ int sl[kLook + kWindow];            // slots of tokens t0 - kLook .. t0 + 2 tile
-  __shared__ uint32_t rows[kWindow];             // row of the token's slot for head 0, kNoRow: skipped
-  __shared__ uint32_t lead[kMaxTile / 32];       // bit x: a run starts at token t0 + x
-  __shared__ uint8_t run_id[kMaxTile];           // run of token t0 + x: the starts up to it, less 1
-  __shared__ uint32_t run_top[kAppWarps][kMaxTile];   // largest magnitude of a run, then its scale, as bits
+  constexpr int PIECES = (int)sizeof(Raw8<IN>) / 16;
+  extern __shared__ __align__(128) char kept[];   // [kTileWarps][hold][PIECES * 512], then:
+  uint2* const rows = reinterpret_cast<uint2*>(kept + kTileWarps * hold * PIECES * 512);   // [2 tile + 16] row of the token's
+                                                  // slot for head 0 (kNoRow: skipped), and its run
+  uint32_t* const run_top = reinterpret_cast<uint32_t*>(rows + 2 * tile + 16);   // [kTileWarps][tile] largest magnitude
+                                                  // of a run, then its scale, as bits
+  int* const sl = reinterpret_cast<int*>(run_top + kTileWarps * tile);   // [kLook + 2 tile] slots of tokens t0 - kLook ..
+  __shared__ uint32_t lead[kMaxTile / 32];        // bit x: a run starts at token t0 + x
+  __shared__ int flags[kTileWarps][2];            // of a set: an infinity or NaN met; a scale that is no power of two
   __shared__ int end_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int set = blockIdx.x % groups * kAppWarps + warp;
+  const int mine = warp / wps, part = warp - mine * wps;   // the warp's set in the CTA, and its part of the rows
+  const int set = blockIdx.x % groups * (kTileWarps / wps) + mine;
+  const bool active = set < 2 * a.c.Hkv;
   const A ap(a, min(set, 2 * a.c.Hkv - 1));
   const int t0 = blockIdx.x / groups * tile;
   const int ps = a.c.page_shift;
-  for (int x = tid; x < kLook + 2 * tile; x += kAppThreads) {
+  for (int x = tid; x < kLook + 2 * tile; x += kTileThreads) {
     const int t = t0 - kLook + x;
     const int slot = t >= 0 && t < a.T ? __ldg(a.slots + t) : -1;
     const bool ok = ap.valid(slot);
     sl[x] = slot;
     if (x >= kLook) {
-      rows[x - kLook] = ok ? q8_row((uint32_t)slot >> ps, (uint32_t)slot & ((1u << ps) - 1u), 0, a.c.Hkv, ps) : kNoRow;
+      rows[x - kLook].x = ok ? q8_row((uint32_t)slot >> ps, (uint32_t)slot & ((1u << ps) - 1u), 0, a.c.Hkv, ps) : kNoRow;
       if (slot != -1 && !ok && x < kLook + tile) raise_error(a.err, kErrPage);
     }
   }
   __syncthreads();
-  if (tid < tile) {   // (tiles are whole warps)
-    bool starts = rows[tid] != kNoRow;
+  for (int x = tid; x < tile; x += kTileThreads) {   // (tiles are whole warps)
+    bool starts = rows[x].x != kNoRow;
     if (starts)
       for (int k = 1; k <= kLook; ++k)
-        if (ap.valid(sl[kLook + tid - k])) {
-          starts = ap.block_of(sl[kLook + tid - k]) != ap.block_of(sl[kLook + tid]);
+        if (ap.valid(sl[kLook + x - k])) {
+          starts = ap.block_of(sl[kLook + x - k]) != ap.block_of(sl[kLook + x]);
           break;
         }
     const uint32_t m = __ballot_sync(0xffffffffu, starts);
-    if (lane == 0) lead[warp] = m;
+    if (lane == 0) lead[x / 32] = m;
   }
   __syncthreads();
-  int x_s = tile, x_l = 0, runs = 0, before = 0;   // first and last start, starts, and those of the words before this warp's
+  int x_s = tile, x_l = 0, runs = 0;   // first and last start, and how many
   for (int w = 0; w < tile / 32; ++w) {
     const uint32_t m = lead[w];
-    if (w < warp) before += __popc(m);
+    // a token's run: the starts up to it, less 1
+    if (w % kTileWarps == warp) rows[32 * w + lane].y = runs + __popc(m & (0xffffffffu >> (31 - lane))) - 1;
     if (m) {
       x_s = min(x_s, 32 * w + __ffs(m) - 1);
       x_l = 32 * w + 31 - __clz(m);
       runs += __popc(m);
     }
   }
-  if (runs == 0) return;
-  if (tid < tile) run_id[tid] = (uint8_t)(before + __popc(lead[warp] & (0xffffffffu >> (31 - lane))) - 1);
-  if (warp == 0) {   // the last run may end behind the tile
+  if (runs == 0) return;   // (the same for every warp)
+  for (int x = tile + tid; x < 2 * tile; x += kTileThreads) rows[x].y = runs - 1;   // (what is left of the last)
+  if (warp == 0) {         // the last run may end behind the tile
     const int n = ap.run_length(t0 + x_l, ap.block_of(sl[kLook + x_l]));
     if (lane == 0) end_s = x_l + n;
   }
-  for (int r = lane; r < runs; r += 32) run_top[warp][r] = 0;
+  uint32_t* const top = run_top + mine * tile;
+  if (part == 0) {
+    for (int r = lane; r < runs; r += 32) top[r] = 0;
+    if (lane < 2) flags[mine][lane] = 0;
+  }
   __syncthreads();
-  if (set >= 2 * a.c.Hkv) return;
-  const int end = end_s, first = x_s + lane / A::LPR;
+  if (!active) return;
+  // from here on a set's warps go on by themselves
+  auto sync_set = [&]() {
+    if (wps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;\n" ::"r"(1 + mine), "r"(wps * 32) : "memory");
+  };
+  auto any_of_set = [&](bool p, int which) -> bool {   // (a barrier of the set too)
+    p = __any_sync(0xffffffffu, p);
+    if (wps > 1) {
+      if (p && lane == 0) flags[mine][which] = 1;
+      sync_set();
+      return flags[mine][which] != 0;
+    }
+    __syncwarp();
+    return p;
+  };
+  const int end = end_s;
+  const int step = wps * A::RPW, first = x_s + part * A::RPW + lane / A::LPR;
+  const int passes = (end - x_s + step - 1) / step;   // rows of a lane
   const uint32_t head_row = (uint32_t)ap.h << ps;
   // row of token t0 + x (past the window only where many are skipped)
   auto row_at = [&](int x) -> uint32_t {
-    if (x < 2 * tile) return rows[x];
+    if (x >= end) return kNoRow;
+    if (x < 2 * tile) return rows[x].x;
     const int slot = __ldg(a.slots + t0 + x);
     return ap.valid(slot) ? q8_row((uint32_t)slot >> ps, (uint32_t)slot & ((1u << ps) - 1u), 0, a.c.Hkv, ps) : kNoRow;
   };
-  auto run_of = [&](int x) -> int { return run_id[min(x, tile - 1)]; };
-  // f(row, values, token) of every row, BATCH loads under way together
-  auto for_rows = [&](auto&& f) {
-    for (int x0 = first; x0 < end; x0 += BATCH * A::RPW) {
-      Raw8<IN> v[BATCH];
-      uint32_t r[BATCH];
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        const int x = x0 + u * A::RPW;
-        r[u] = x < end ? row_at(x) : kNoRow;
-        if (r[u] != kNoRow) v[u] = ap.load(t0 + x);
-      }
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u)
-        if (r[u] != kNoRow) f(r[u], v[u], x0 + u * A::RPW);
-    }
-  };
-  // f(values, token) of every row where none is skipped: no test per row (past
-  // the end the last row again)
-  auto for_all = [&](auto&& f) {
-    for (int x0 = first; x0 < end; x0 += BATCH * A::RPW) {
-      Raw8<IN> v[BATCH];
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u) v[u] = ap.load(t0 + min(x0 + u * A::RPW, end - 1));
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u) f(v[u], x0 + u * A::RPW);
-    }
-  };
-  // one run and no skipped row in sight: the case of a prompt
-  bool plain = runs == 1 && end <= 2 * tile;
-  for (int x = x_s + lane; plain && x < end; x += 32) plain = rows[x] != kNoRow;
+  auto run_of = [&](int x) -> int { return (int)rows[min(x, tile - 1)].y; };
+  bool plain = end <= 2 * tile;   // no row is skipped: no test per row
+  for (int x = x_s + lane; plain && x < end; x += 32) plain = rows[x].x != kNoRow;
   plain = __all_sync(0xffffffffu, plain);
-  // maxima: of all rows at once, or joined row by row
-  if (plain) {
-    MaxAcc<IN> acc;
-    for_all([&](const Raw8<IN>& v, int) { acc.add(v); });
-    if (__any_sync(0xffffffffu, !acc.finite())) {
-      acc.m = 0;
-      for_rows([&](uint32_t, const Raw8<IN>& v, int) { acc.add_finite(v); });
-    }
-    const uint32_t m = __reduce_max_sync(0xffffffffu, acc.bits());
-    if (lane == 0) run_top[warp][0] = m;
-  } else {
-    for_rows([&](uint32_t, const Raw8<IN>& v, int x) {
-      MaxAcc<IN> acc;
-      acc.add(v);
-      if (!acc.finite()) {
-        acc.m = 0;
-        acc.add_finite(v);
+  // Rows come to shared memory hold passes at a time.  The lanes of a row copy
+  // 16 bytes next to one another (whole sectors), which for fp32 are not all
+  // the columns that they work on: those lie where kept_at finds them.
+  const int chunks = (passes + hold - 1) / hold, l = lane % A::LPR;
+  const char* const home = kept + warp * hold * PIECES * 512 + lane * 16;
+  const uint32_t to = smem_u32(home) + (PIECES == 2 ? ((l & 1) * 32 + (l >> 1) - l) * 16 : 0);
+  int here = -1;                  // the chunk that is in shared memory
+  auto fetch = [&](int c) -> int {   // returns the chunk's passes
+    const int p0 = c * hold, n = min(hold, passes - p0);
+    if (c == here) return n;
+    here = c;
+    __syncwarp();
+    auto copy = [&](int q, const char* from, int bytes) {
+#pragma unroll
+      for (int w = 0; w < PIECES; ++w)
+        cp_async_16(to + q * PIECES * 512 + w * A::LPR * 8, from - (PIECES - 1) * l * 16 + w * A::LPR * 16, bytes);
+    };
+    if (plain) {
+      const char* from = ap.address(t0 + first + p0 * step);
+      const int64_t skip = step * ap.token_bytes();
+#pragma unroll 4
+      for (int q = 0; q < n - 1; ++q, from += skip) copy(q, from, 16);
+      copy(n - 1, ap.address(t0 + min(first + (p0 + n - 1) * step, end - 1)), 16);   // (past the end the last row again)
+    } else {
+      for (int q = 0; q < n; ++q) {   // zeros for skipped rows and past the end
+        const int x = first + (p0 + q) * step;
+        const bool have = row_at(x) != kNoRow;
+        copy(q, ap.address(have ? t0 + x : t0), have ? 16 : 0);
       }
-      atomicMax(&run_top[warp][run_of(x)], acc.bits());
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncwarp();
+    return n;
+  };
+  auto kept_at = [&](int q) -> Raw8<IN> {
+    Raw8<IN> r;
+#pragma unroll
+    for (int w = 0; w < PIECES; ++w) r.w[w] = *reinterpret_cast<const uint4*>(home + (q * PIECES + w) * 512);
+    return r;
+  };
+  // f(chunk's first pass, its passes) over all rows, the chunk that is here first
+  auto sweep = [&](auto&& f) {
+    const int c0 = max(here, 0), dir = c0 > 0 ? -1 : 1;
+    for (int i = 0, c = c0; i < chunks; ++i, c += dir) {
+      const int n = fetch(c);
+      f(c * hold, n);
+    }
+  };
+  // f(values, token) of every row; skipped ones are zeros
+  auto for_rows = [&](auto&& f) {
+    sweep([&](int p0, int n) {
+#pragma unroll 2
+      for (int q = 0; q < n; ++q) f(kept_at(q), first + (p0 + q) * step);
     });
+  };
+  // maxima: a lane keeps its own while its rows stay in one run; the lanes of a
+  // row (which change runs together) join theirs before the shared maximum
+  const uint32_t row_lanes = ((1u << A::LPR) - 1u) << (lane / A::LPR * A::LPR);
+  const bool single = plain && runs == 1;   // the case of a prompt
+  bool odd = false;                         // an infinity or NaN was met
+  auto maxima = [&](bool finite_only) {
+    MaxAcc<IN> acc;
+    int cur = run_of(first);
+    auto flush = [&]() {
+      odd |= !acc.finite();
+      const uint32_t m = __reduce_max_sync(row_lanes, acc.bits());
+      if (lane % A::LPR == 0) atomicMax(top + cur, m);
+      acc.m = 0;
+    };
+    if (single && !finite_only) {
+      sweep([&](int, int n) {
+#pragma unroll 4
+        for (int q = 0; q < n; ++q) acc.add(kept_at(q));
+      });
+    } else if (plain && !finite_only) {
+      sweep([&](int p0, int n) {   // (the last pass may be past the end: the last row again, of its run)
+        const uint2* row = rows + first + p0 * step;
+#pragma unroll 2
+        for (int q = 0; q < n; ++q, row += step) {
+          const int r = q < n - 1 ? (int)row->y : run_of(min(first + (p0 + q) * step, end - 1));
+          if (r != cur) {
+            flush();
+            cur = r;
+          }
+          acc.add(kept_at(q));
+        }
+      });
+    } else {
+      for_rows([&](const Raw8<IN>& v, int x) {
+        const int r = run_of(x);
+        if (r != cur) {
+          flush();
+          cur = r;
+        }
+        if (finite_only) acc.add_finite(v);
+        else acc.add(v);
+      });
+    }
+    flush();
+  };
+  maxima(false);
+  if (any_of_set(odd, 0)) {   // once more without them
+    if (part == 0)
+      for (int r = lane; r < runs; r += 32) top[r] = 0;
+    sync_set();
+    maxima(true);
+    sync_set();
   }
-  __syncwarp();
   // scales, a lane per run; rows before a run whose scale grew, by the warp
-  for (int x0 = 0; x0 < tile; x0 += 32) {
-    const int x = x0 + lane;
-    const bool starts = lead[x0 / 32] >> lane & 1u;
-    float ratio = 1.0f;
-    uint32_t row = 0, offset = 0;
-    if (starts) {   // token t0 + x starts a run
-      const int r = run_id[x];
-      offset = ap.offset_in_block(sl[kLook + x]);
-      row = rows[x] + head_row;
-      float* sp = ap.scale_at(row);
-      const float s = ap.new_scale(run_top[warp][r], offset, offset ? *sp : 0.0f, ratio);
-      *sp = s;
-      run_top[warp][r] = __float_as_uint(s);
-    }
-    for (uint32_t grew = __ballot_sync(0xffffffffu, ratio != 1.0f); grew; grew &= grew - 1) {
-      const int l = __ffs(grew) - 1;
-      const uint32_t n = __shfl_sync(0xffffffffu, offset, l);
-      ap.requant(__shfl_sync(0xffffffffu, row, l) - n, (int)n, __shfl_sync(0xffffffffu, ratio, l), lane, 32);
+  bool pow2 = true;
+  if (part == 0) {
+    for (int x0 = 0; x0 < tile; x0 += 32) {
+      const int x = x0 + lane;
+      const bool starts = lead[x0 / 32] >> lane & 1u;
+      float ratio = 1.0f;
+      uint32_t row = 0, offset = 0;
+      if (starts) {   // token t0 + x starts a run
+        const int r = (int)rows[x].y;
+        offset = ap.offset_in_block(sl[kLook + x]);
+        row = rows[x].x + head_row;
+        float* sp = ap.scale_at(row);
+        const float s = ap.new_scale(top[r], offset, offset ? *sp : 0.0f, ratio);
+        *sp = s;
+        top[r] = __float_as_uint(s);
+        pow2 &= is_pow2(s);
+      }
+      for (uint32_t grew = __ballot_sync(0xffffffffu, ratio != 1.0f); grew; grew &= grew - 1) {
+        const int l = __ffs(grew) - 1;
+        const uint32_t n = __shfl_sync(0xffffffffu, offset, l);
+        ap.requant(__shfl_sync(0xffffffffu, row, l) - n, (int)n, __shfl_sync(0xffffffffu, ratio, l), lane, 32);
+      }
     }
   }
-  __syncwarp();
-  const float s0 = __uint_as_float(run_top[warp][0]);
-  if (plain && is_pow2(s0)) {
-    const float inv = 1.0f / s0;
-    for_all([&](const Raw8<IN>& v, int x) {
-      const uint2 y = pack8_pow2<IN, CT>(v, inv);
-      if (x < end) *reinterpret_cast<uint2*>(ap.pages + (size_t)(rows[x] + head_row) * D + ap.col) = y;
+  uint8_t* const pages = ap.pages + (size_t)head_row * D + ap.col;
+  if (any_of_set(!pow2, 1)) {
+    for_rows([&](const Raw8<IN>& v, int x) {
+      const uint32_t r = row_at(x);
+      if (r != kNoRow) ap.store_row(r + head_row, v, __uint_as_float(top[run_of(x)]));
+    });
+  } else if (plain) {
+    const float inv = 1.0f / __uint_as_float(top[0]);
+    sweep([&](int p0, int n) {
+      const uint2* row = rows + first + p0 * step;
+      if (runs == 1) {
+#pragma unroll 4
+        for (int q = 0; q < n - 1; ++q, row += step)
+          *reinterpret_cast<uint2*>(pages + (size_t)row->x * D) = pack8_pow2<IN, CT>(kept_at(q), inv);
+      } else {
+#pragma unroll 4
+        for (int q = 0; q < n - 1; ++q, row += step) {
+          const uint2 r = *row;
+          // 1 / s by its exponent: s = 2^e, |e| <= 122
+          const float inv_r = __uint_as_float((254u << 23) - top[r.y]);
+          *reinterpret_cast<uint2*>(pages + (size_t)r.x * D) = pack8_pow2<IN, CT>(kept_at(q), inv_r);
+        }
+      }
+      if (first + (p0 + n - 1) * step < end)
+        *reinterpret_cast<uint2*>(pages + (size_t)row->x * D) =
+            pack8_pow2<IN, CT>(kept_at(n - 1), 1.0f / __uint_as_float(top[row->y]));
     });
   } else {
-    for_rows([&](uint32_t r, const Raw8<IN>& v, int x) {
-      ap.store_row(r + head_row, v, __uint_as_float(run_top[warp][run_of(x)]));
+    for_rows([&](const Raw8<IN>& v, int x) {
+      const uint32_t r = row_at(x);
+      const uint2 y = pack8_pow2<IN, CT>(v, 1.0f / __uint_as_float(top[run_of(x)]));
+      if (r != kNoRow) *reinterpret_cast<uint2*>(pages + (size_t)r * D) = y;
     });
   }
 }
@@ -702,16 +869,32 @@ __global__ void __launch_bounds__(kGatThreads) q8_gather_kernel(const Q8GatherAr
 
 template <int D, int IN, int CT>
 cudaError_t run_append(const Q8AppendArgs& a, cudaStream_t st) {
-  // a token per warp as long as that is not many CTAs, as in a decode step;
-  // else tiles of a block's size, so that a prompt's runs start one to a tile
+  // rows by themselves; a token per warp as long as that is not many CTAs, as
+  // in a decode step; else tiles of a block's size, so that a prompt's runs
+  // start one to a tile
   const int sets = 2 * a.c.Hkv;
+  if (a.c.block_shift == 0) {
+    const int rows = kAppThreads / (D / 8) * kRowBatch;
+    const int64_t ctas = ((int64_t)a.T * sets + rows - 1) / rows;
+    return launch_ex(q8_append_rows_kernel<D, IN, CT>, dim3((unsigned)ctas), dim3(kAppThreads), 0, st, false, 1, a);
+  }
   const int64_t few = ((int64_t)a.T + kAppWarps - 1) / kAppWarps * sets;
   if (few <= kFewCtas)
     return launch_ex(q8_append_kernel<D, IN, CT>, dim3((unsigned)few), dim3(kAppThreads), 0, st, false, 1, a);
-  const int tile = min(max(1 << a.c.block_shift, 64), kMaxTile), groups = (sets + kAppWarps - 1) / kAppWarps;
+  // as many warps to a (head, tensor) as hold a tile's rows: a block's where a
+  // run is a tile, else the tile's and those of a run that reaches over its end
+  constexpr int ROW = D * (IN == kInF32 ? 4 : 2), PASS = IN == kInF32 ? 1024 : 512;   // bytes of a row, and a warp's pass
+  const int block = 1 << a.c.block_shift, tile = min(max(block, 64), kMaxTile);
+  const int window = (block >= tile ? tile : tile + block) * ROW;
+  const int wps = window <= kKept ? 1 : window <= 2 * kKept ? 2 : 4;
+  const int hold = min(window / wps, kKept) / PASS;
+  const int per_cta = kTileWarps / wps, groups = (sets + per_cta - 1) / per_cta;
   const int64_t ctas = ((int64_t)a.T + tile - 1) / tile * groups;
-  return launch_ex(q8_append_tiled_kernel<D, IN, CT>, dim3((unsigned)ctas), dim3(kAppThreads), 0, st, false, 1, a, tile,
-                   groups);
+  const auto fn = q8_append_tiled_kernel<D, IN, CT>;
+  const size_t smem = (size_t)kTileWarps * hold * PASS + (2 * tile + 16) * 8 + kTileWarps * tile * 4 + (kLook + 2 * tile) * 4;
+  const cudaError_t e = ensure_func_attrs(reinterpret_cast<const void*>(fn), smem, false);
+  if (e != cudaSuccess) return e;
+  return launch_ex(fn, dim3((unsigned)ctas), dim3(kTileThreads), smem, st, false, 1, a, tile, groups, wps, hold);
 }
 
 template <int D, int CT>
