@@ -364,11 +364,12 @@ struct Appender {
   }
   // tokens of the run that starts at token t: to the last one before a token of
   // another block or kLook skipped ones (a whole warp)
-  __device__ int run_length(int t, uint32_t blk) const {
+  // the slots of tokens t .. t + have - 1 are in near
+  __device__ int run_length(int t, uint32_t blk, const int* near = nullptr, int have = 0) const {
     int n = 1;
     for (;;) {
-      const int u = t + n + (int)(threadIdx.x & 31);
-      const int y = u < a.T ? __ldg(a.slots + u) : -1;
+      const int i = n + (int)(threadIdx.x & 31), u = t + i;
+      const int y = i < have ? near[i] : u < a.T ? __ldg(a.slots + u) : -1;
       const bool ok = valid(y), here = ok && block_of(y) == blk;
       uint32_t in = __ballot_sync(0xffffffffu, here);
       const uint32_t other = __ballot_sync(0xffffffffu, ok && !here);
@@ -546,6 +547,94 @@ __global__ void __launch_bounds__(kTileThreads, 5)
   const A ap(a, min(set, 2 * a.c.Hkv - 1));
   const int t0 = blockIdx.x / groups * tile;
   const int ps = a.c.page_shift;
+  // a set's warps go on by themselves once they know their runs
+  auto sync_set = [&]() {
+    if (wps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;\n" ::"r"(1 + mine), "r"(wps * 32) : "memory");
+  };
+  auto any_of_set = [&](bool p, int which) -> bool {   // (a barrier of the set too)
+    p = __any_sync(0xffffffffu, p);
+    if (wps > 1) {
+      if (p && lane == 0) flags[mine][which] = 1;
+      sync_set();
+      return flags[mine][which] != 0;
+    }
+    __syncwarp();
+    return p;
+  };
+  // the warp's passes: rows sub, sub + step ..
+  const int step = wps * A::RPW, sub = part * A::RPW + lane / A::LPR;
+  uint32_t* const top = run_top + mine * tile;
+  const uint32_t head_row = (uint32_t)ap.h << ps;
+  uint8_t* const pages = ap.pages + (size_t)head_row * D + ap.col;
+  // The lanes of a row copy 16 bytes next to one another (whole sectors), which
+  // for fp32 are not all the columns that they work on: kept_at finds those.
+  const int l = lane % A::LPR;
+  const char* const home = kept + warp * hold * PIECES * 512 + lane * 16;
+  const uint32_t to = smem_u32(home) + (PIECES == 2 ? ((l & 1) * 32 + (l >> 1) - l) * 16 : 0);
+  auto copy = [&](int q, const char* from, int bytes) {
+#pragma unroll
+    for (int w = 0; w < PIECES; ++w)
+      cp_async_16(to + q * PIECES * 512 + w * A::LPR * 8, from - (PIECES - 1) * l * 16 + w * A::LPR * 16, bytes);
+  };
+  auto kept_at = [&](int q) -> Raw8<IN> {
+    Raw8<IN> r;
+#pragma unroll
+    for (int w = 0; w < PIECES; ++w) r.w[w] = *reinterpret_cast<const uint4*>(home + (q * PIECES + w) * 512);
+    return r;
+  };
+
+  // Whole blocks, in order, from token x_s on (a prompt, once past its first
+  // block): their rows follow one another, and there is no earlier scale.
+  const int shift = a.c.block_shift, block = 1 << shift;
+  {
+    const int x_s = (int)((0u - (uint32_t)__ldg(a.slots + t0)) & (uint32_t)(block - 1));
+    bool whole = t0 + x_s + tile <= a.T && block >= step && tile <= hold * step;
+    if (whole)
+      for (int x = tid; x < x_s + tile; x += kTileThreads) {   // (those before x_s go on with a run from before)
+        const int slot = __ldg(a.slots + t0 + x), before = t0 + x > 0 ? __ldg(a.slots + t0 + x - 1) : -1;
+        const int o = (int)ap.offset_in_block(slot);
+        whole &= ap.valid(slot) && o == ((x - x_s) & (block - 1)) && (o == 0 || slot - 1 == before);
+        if (whole && x >= x_s && o == 0)
+          rows[(x - x_s) >> shift].x = q8_row((uint32_t)slot >> ps, (uint32_t)slot & ((1u << ps) - 1u), 0, a.c.Hkv, ps);
+      }
+    if (part == 0)
+      for (int r = lane; r < tile >> shift; r += 32) top[r] = 0;
+    if (__syncthreads_and(whole)) {
+      if (!active) return;
+      const char* from = ap.address(t0 + x_s + sub);
+      const int64_t skip = step * ap.token_bytes();
+      const int n = block / step, runs = tile >> shift;
+#pragma unroll 4
+      for (int q = 0; q < tile / step; ++q, from += skip) copy(q, from, 16);
+      cp_async_commit();
+      cp_async_wait<0>();
+      __syncwarp();
+      for (int r = 0; r < runs; ++r) {
+        MaxAcc<IN> acc;
+#pragma unroll 4
+        for (int q = r * n; q < (r + 1) * n; ++q) acc.add(kept_at(q));
+        if (__any_sync(0xffffffffu, !acc.finite())) {
+          acc.m = 0;
+          for (int q = r * n; q < (r + 1) * n; ++q) acc.add_finite(kept_at(q));
+        }
+        const uint32_t m = __reduce_max_sync(0xffffffffu, acc.bits());
+        if (lane == 0) atomicMax(top + r, m);
+      }
+      sync_set();
+      for (int r = 0; r < runs; ++r) {
+        float ratio;
+        const float s = ap.new_scale(top[r], 0, 0.0f, ratio), inv = 1.0f / s;
+        const uint32_t row = rows[r].x;
+        if (part == 0 && lane == 0) *ap.scale_at(row + head_row) = s;
+        uint8_t* out = pages + (size_t)(row + sub) * D;
+#pragma unroll 4
+        for (int q = r * n; q < (r + 1) * n; ++q, out += step * D)
+          *reinterpret_cast<uint2*>(out) = pack8_pow2<IN, CT>(kept_at(q), inv);
+      }
+      return;
+    }
+  }
   for (int x = tid; x < kLook + 2 * tile; x += kTileThreads) {
     const int t = t0 - kLook + x;
     const int slot = t >= 0 && t < a.T ? __ldg(a.slots + t) : -1;
@@ -583,35 +672,18 @@ __global__ void __launch_bounds__(kTileThreads, 5)
   if (runs == 0) return;   // (the same for every warp)
   for (int x = tile + tid; x < 2 * tile; x += kTileThreads) rows[x].y = runs - 1;   // (what is left of the last)
   if (warp == 0) {         // the last run may end behind the tile
-    const int n = ap.run_length(t0 + x_l, ap.block_of(sl[kLook + x_l]));
+    const int n = ap.run_length(t0 + x_l, ap.block_of(sl[kLook + x_l]), sl + kLook + x_l, 2 * tile - x_l);
     if (lane == 0) end_s = x_l + n;
   }
-  uint32_t* const top = run_top + mine * tile;
   if (part == 0) {
     for (int r = lane; r < runs; r += 32) top[r] = 0;
     if (lane < 2) flags[mine][lane] = 0;
   }
   __syncthreads();
   if (!active) return;
-  // from here on a set's warps go on by themselves
-  auto sync_set = [&]() {
-    if (wps == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;\n" ::"r"(1 + mine), "r"(wps * 32) : "memory");
-  };
-  auto any_of_set = [&](bool p, int which) -> bool {   // (a barrier of the set too)
-    p = __any_sync(0xffffffffu, p);
-    if (wps > 1) {
-      if (p && lane == 0) flags[mine][which] = 1;
-      sync_set();
-      return flags[mine][which] != 0;
-    }
-    __syncwarp();
-    return p;
-  };
   const int end = end_s;
-  const int step = wps * A::RPW, first = x_s + part * A::RPW + lane / A::LPR;
+  const int first = x_s + sub;
   const int passes = (end - x_s + step - 1) / step;   // rows of a lane
-  const uint32_t head_row = (uint32_t)ap.h << ps;
   // row of token t0 + x (past the window only where many are skipped)
   auto row_at = [&](int x) -> uint32_t {
     if (x >= end) return kNoRow;
@@ -623,23 +695,14 @@ __global__ void __launch_bounds__(kTileThreads, 5)
   bool plain = end <= 2 * tile;   // no row is skipped: no test per row
   for (int x = x_s + lane; plain && x < end; x += 32) plain = rows[x].x != kNoRow;
   plain = __all_sync(0xffffffffu, plain);
-  // Rows come to shared memory hold passes at a time.  The lanes of a row copy
-  // 16 bytes next to one another (whole sectors), which for fp32 are not all
-  // the columns that they work on: those lie where kept_at finds them.
-  const int chunks = (passes + hold - 1) / hold, l = lane % A::LPR;
-  const char* const home = kept + warp * hold * PIECES * 512 + lane * 16;
-  const uint32_t to = smem_u32(home) + (PIECES == 2 ? ((l & 1) * 32 + (l >> 1) - l) * 16 : 0);
+  // rows come to shared memory hold passes at a time
+  const int chunks = (passes + hold - 1) / hold;
   int here = -1;                  // the chunk that is in shared memory
   auto fetch = [&](int c) -> int {   // returns the chunk's passes
     const int p0 = c * hold, n = min(hold, passes - p0);
     if (c == here) return n;
     here = c;
     __syncwarp();
-    auto copy = [&](int q, const char* from, int bytes) {
-#pragma unroll
-      for (int w = 0; w < PIECES; ++w)
-        cp_async_16(to + q * PIECES * 512 + w * A::LPR * 8, from - (PIECES - 1) * l * 16 + w * A::LPR * 16, bytes);
-    };
     if (plain) {
       const char* from = ap.address(t0 + first + p0 * step);
       const int64_t skip = step * ap.token_bytes();
@@ -657,12 +720,6 @@ __global__ void __launch_bounds__(kTileThreads, 5)
     cp_async_wait<0>();
     __syncwarp();
     return n;
-  };
-  auto kept_at = [&](int q) -> Raw8<IN> {
-    Raw8<IN> r;
-#pragma unroll
-    for (int w = 0; w < PIECES; ++w) r.w[w] = *reinterpret_cast<const uint4*>(home + (q * PIECES + w) * 512);
-    return r;
   };
   // f(chunk's first pass, its passes) over all rows, the chunk that is here first
   auto sweep = [&](auto&& f) {
@@ -682,7 +739,6 @@ __global__ void __launch_bounds__(kTileThreads, 5)
   // maxima: a lane keeps its own while its rows stay in one run; the lanes of a
   // row (which change runs together) join theirs before the shared maximum
   const uint32_t row_lanes = ((1u << A::LPR) - 1u) << (lane / A::LPR * A::LPR);
-  const bool single = plain && runs == 1;   // the case of a prompt
   bool odd = false;                         // an infinity or NaN was met
   auto maxima = [&](bool finite_only) {
     MaxAcc<IN> acc;
@@ -693,12 +749,7 @@ __global__ void __launch_bounds__(kTileThreads, 5)
       if (lane % A::LPR == 0) atomicMax(top + cur, m);
       acc.m = 0;
     };
-    if (single && !finite_only) {
-      sweep([&](int, int n) {
-#pragma unroll 4
-        for (int q = 0; q < n; ++q) acc.add(kept_at(q));
-      });
-    } else if (plain && !finite_only) {
+    if (plain && !finite_only) {
       sweep([&](int p0, int n) {   // (the last pass may be past the end: the last row again, of its run)
         const uint2* row = rows + first + p0 * step;
 #pragma unroll 2
@@ -757,28 +808,20 @@ __global__ void __launch_bounds__(kTileThreads, 5)
       }
     }
   }
-  uint8_t* const pages = ap.pages + (size_t)head_row * D + ap.col;
   if (any_of_set(!pow2, 1)) {
     for_rows([&](const Raw8<IN>& v, int x) {
       const uint32_t r = row_at(x);
       if (r != kNoRow) ap.store_row(r + head_row, v, __uint_as_float(top[run_of(x)]));
     });
   } else if (plain) {
-    const float inv = 1.0f / __uint_as_float(top[0]);
     sweep([&](int p0, int n) {
       const uint2* row = rows + first + p0 * step;
-      if (runs == 1) {
 #pragma unroll 4
-        for (int q = 0; q < n - 1; ++q, row += step)
-          *reinterpret_cast<uint2*>(pages + (size_t)row->x * D) = pack8_pow2<IN, CT>(kept_at(q), inv);
-      } else {
-#pragma unroll 4
-        for (int q = 0; q < n - 1; ++q, row += step) {
-          const uint2 r = *row;
-          // 1 / s by its exponent: s = 2^e, |e| <= 122
-          const float inv_r = __uint_as_float((254u << 23) - top[r.y]);
-          *reinterpret_cast<uint2*>(pages + (size_t)r.x * D) = pack8_pow2<IN, CT>(kept_at(q), inv_r);
-        }
+      for (int q = 0; q < n - 1; ++q, row += step) {
+        const uint2 r = *row;
+        // 1 / s by its exponent: s = 2^e, |e| <= 122
+        const float inv = __uint_as_float((254u << 23) - top[r.y]);
+        *reinterpret_cast<uint2*>(pages + (size_t)r.x * D) = pack8_pow2<IN, CT>(kept_at(q), inv);
       }
       if (first + (p0 + n - 1) * step < end)
         *reinterpret_cast<uint2*>(pages + (size_t)row->x * D) =
