@@ -159,7 +159,7 @@ constexpr int kAppThreads = 256;
 constexpr int kAppWarps = kAppThreads / 32;
 constexpr int kShortRun = 8;   // rows of a run that a warp does alone
 constexpr int kMaxTile = 256;
-constexpr int kFewCtas = 4096;
+constexpr int kFewCtas = 2048;
 constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr int kLook = 32;      // skipped tokens that part two runs of one block
 
@@ -383,31 +383,31 @@ struct Appender {
 // One scale per row (S = 1): rows have nothing to do with one another.  The lanes
 // of a row read it, find its maximum and scale, and write it, from registers;
 // kRowBatch rows per lane under way together.
-constexpr int kRowBatch = 4;
+constexpr int kRowBatch = 2;
 template <int D, int IN, int CT>
 __global__ void __launch_bounds__(kAppThreads) q8_append_rows_kernel(const Q8AppendArgs a) {
   using A = Appender<D, IN, CT>;
   constexpr int GROUPS = kAppThreads / A::LPR;
   const int sets = 2 * a.c.Hkv, total = a.T * sets;   // (31 bits: checked on the host)
-  const int u0 = blockIdx.x * (GROUPS * kRowBatch) + (int)threadIdx.x / A::LPR;
+  int u = blockIdx.x * (GROUPS * kRowBatch) + (int)threadIdx.x / A::LPR;
   const int lane = threadIdx.x & 31;
   const uint32_t row_lanes = ((1u << A::LPR) - 1u) << (lane / A::LPR * A::LPR);
   Raw8<IN> v[kRowBatch];
-  int slot[kRowBatch];
+  int slot[kRowBatch], t[kRowBatch];
 #pragma unroll
-  for (int i = 0; i < kRowBatch; ++i) {   // neighbouring lanes: the heads of a token
-    const int u = u0 + i * GROUPS;
+  for (int i = 0; i < kRowBatch; ++i, u += GROUPS) {   // neighbouring lanes: the heads of a token
+    t[i] = u / sets;
     slot[i] = -1;
     if (u < total) {
-      const A ap(a, u % sets);
-      slot[i] = __ldg(a.slots + u / sets);
-      v[i] = ap.load(u / sets);
+      const A ap(a, u - t[i] * sets);
+      slot[i] = __ldg(a.slots + t[i]);
+      v[i] = ap.load(t[i]);
     }
   }
+  u -= kRowBatch * GROUPS;
 #pragma unroll
-  for (int i = 0; i < kRowBatch; ++i) {
-    const int u = u0 + i * GROUPS;
-    const A ap(a, u % sets);
+  for (int i = 0; i < kRowBatch; ++i, u += GROUPS) {
+    const A ap(a, u - t[i] * sets);
     if (!ap.valid(slot[i])) {   // (the lanes of a row agree)
       if (slot[i] != -1) raise_error(a.err, kErrPage);
       continue;
@@ -568,19 +568,29 @@ __global__ void __launch_bounds__(kTileThreads, 5)
   const uint32_t head_row = (uint32_t)ap.h << ps;
   uint8_t* const pages = ap.pages + (size_t)head_row * D + ap.col;
   // The lanes of a row copy 16 bytes next to one another (whole sectors), which
-  // for fp32 are not all the columns that they work on: kept_at finds those.
+  // for fp32 are not all the columns that they work on: kept_at finds those,
+  // 32 bytes of a row, of which every other four lanes read the second half
+  // first, so that eight lanes meet all banks.
   const int l = lane % A::LPR;
   const char* const home = kept + warp * hold * PIECES * 512 + lane * 16;
-  const uint32_t to = smem_u32(home) + (PIECES == 2 ? ((l & 1) * 32 + (l >> 1) - l) * 16 : 0);
+  const uint32_t to = smem_u32(home);
+  const bool swap = l & 4;
+  const int own = PIECES == 1 ? 0 : (2 * l >= A::LPR ? 512 + (l - A::LPR) * 16 : l * 16) + (swap ? 16 : 0);
   auto copy = [&](int q, const char* from, int bytes) {
 #pragma unroll
     for (int w = 0; w < PIECES; ++w)
-      cp_async_16(to + q * PIECES * 512 + w * A::LPR * 8, from - (PIECES - 1) * l * 16 + w * A::LPR * 16, bytes);
+      cp_async_16(to + (q * PIECES + w) * 512, from - (PIECES - 1) * l * 16 + w * A::LPR * 16, bytes);
   };
   auto kept_at = [&](int q) -> Raw8<IN> {
     Raw8<IN> r;
-#pragma unroll
-    for (int w = 0; w < PIECES; ++w) r.w[w] = *reinterpret_cast<const uint4*>(home + (q * PIECES + w) * 512);
+    const char* const at = home + own + q * PIECES * 512;
+    if constexpr (PIECES == 1) {
+      r.w[0] = *reinterpret_cast<const uint4*>(at);
+    } else {
+      const uint4 x = *reinterpret_cast<const uint4*>(at), y = *reinterpret_cast<const uint4*>(at + (swap ? -16 : 16));
+      r.w[0] = swap ? y : x;
+      r.w[1] = swap ? x : y;
+    }
     return r;
   };
 
