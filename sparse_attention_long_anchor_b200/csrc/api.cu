@@ -847,8 +847,8 @@ int kascade_q8_append(const kascade_q8_cache* c, const void* k, const void* v, i
   if (rc) return rc;
   if (num_tokens < 0) return KASCADE_ERR_INVALID_ARG;
   if (!known_dtype(dtype)) return KASCADE_ERR_UNSUPPORTED;
-  // rows of K and V are numbered in 31 bits
-  if ((int64_t)num_tokens * c->num_kv_heads >= (1ll << 30)) return KASCADE_ERR_UNSUPPORTED;
+  // rows of K and V are numbered in 31 bits (the last CTA's past the end too)
+  if ((int64_t)num_tokens * c->num_kv_heads >= (1ll << 30) - 4096) return KASCADE_ERR_UNSUPPORTED;
   if (num_tokens == 0) return KASCADE_OK;
   if (!k || !v || !slot_map) return KASCADE_ERR_INVALID_ARG;
   const int64_t unit = dtype == KASCADE_DTYPE_F32 ? 4 : 8;   // elements of 16 bytes

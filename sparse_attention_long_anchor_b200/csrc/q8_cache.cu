@@ -146,11 +146,10 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const PageTabl
 //   if rows of the block precede the run: s = max(s_old, s), and where that
 //   grew, those rows become rn(y s_old / s);
 //   the new rows become rn(x / s).
-// Bound by HBM for prompts: each input value is read once from there (a second
-// time from L1 or L2, once its run's maximum is known) and each byte written
-// once: 45 us for a 32K prompt of 8 kv heads, d = 128 in bf16 (4.5 TB/s; a
-// fifth of the second reads miss L2).  A decode step is bound by latency: 2.2
-// us for 8 requests.
+// Bound by HBM for prompts: each input value is read once and waits on the SM
+// for its run's maximum, each byte is written once: 36 us for a 32K prompt of 8
+// kv heads, d = 128 in bf16 (5.6 TB/s), 58 us in fp32 (5.8 TB/s).  A decode
+// step is bound by latency: 2.2 us for 8 requests.
 //
 // Three kernels, by the block's size and the number of tokens (see run_append).
 // The heads of a token are worked on next to one another: together they read
@@ -159,6 +158,10 @@ constexpr int kAppThreads = 256;
 constexpr int kAppWarps = kAppThreads / 32;
 constexpr int kShortRun = 8;   // rows of a run that a warp does alone
 constexpr int kMaxTile = 256;
+// CTAs of the form for few tokens (8 tokens of a set each) up to which it is
+// taken.  8 kv heads, d = 128 in bf16, few against many: decode steps of 512
+// 6.0 and 14.5 us, of 1024 9.9 and 14.4, of 2048 17.7 and 14.6; prompts of 1000
+// tokens 7.7 and 7.1, of 2048 12.0 and 4.4 (8 of 250 13.4 and 13.5).
 constexpr int kFewCtas = 2048;
 constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr int kLook = 32;      // skipped tokens that part two runs of one block
@@ -382,7 +385,8 @@ struct Appender {
 
 // One scale per row (S = 1): rows have nothing to do with one another.  The lanes
 // of a row read it, find its maximum and scale, and write it, from registers;
-// kRowBatch rows per lane under way together.
+// kRowBatch rows per lane under way together.  32K tokens of 8 kv heads, d = 128
+// in bf16: 50 us (83 as runs of one row each).
 constexpr int kRowBatch = 2;
 template <int D, int IN, int CT>
 __global__ void __launch_bounds__(kAppThreads) q8_append_rows_kernel(const Q8AppendArgs a) {
@@ -514,14 +518,17 @@ __global__ void __launch_bounds__(kAppThreads) q8_append_kernel(const Q8AppendAr
 
 // Many tokens (prompts): one, two or four warps take a tile's runs of one (kv
 // head, tensor), all at once whatever their lengths are; the CTA's warps take
-// neighbouring heads of the same tile, whose runs they find together, a token
-// per thread.  Every row from the first start to the end of the last run is
-// read into shared memory, where it waits for its run's scale: the maxima are
-// joined per run (integer maxima: order does not matter), a lane per run finds
-// the scale, then the rows are rounded and written.  (Windows that do not fit,
-// as at a border of two long runs, are read twice instead.)  What a row needs
-// beside its values is found once per CTA: instructions per value bound this
-// kernel as much as its bytes.
+// neighbouring heads of the same tile.  Every row from the first start to the
+// end of the last run is read into shared memory, where it waits for its run's
+// scale: the maxima are joined per run (integer maxima: order does not matter),
+// then the rows are rounded and written.  (A window that does not fit, as at a
+// border of two long runs, comes in chunks, all but one of them twice.)
+// Instructions bound this kernel as much as bytes do: a warp's fixed part, run
+// one after the other, takes as long as its rows.  So a tile of whole blocks in
+// order, the rule in a prompt, is told by one test per token and needs none of
+// the search for runs (32K tokens: 42.8 us with the search, 35.8 without), a
+// CTA has four warps (two: 53 us) and a set as few as hold its rows (two where
+// one does: 49 us).
 constexpr int kTileWarps = 4;
 constexpr int kTileThreads = kTileWarps * 32;
 constexpr int kKept = 16384;   // bytes of shared memory per warp: three CTAs, 192 KB under way per SM

@@ -194,6 +194,46 @@ def test_append_tiled_form_values_gaps_and_old_rows(kind, dtype, d, page, block)
     assert ws.error(clear=True) == kc.DEVERR_PAGE
 
 
+@pytest.mark.parametrize("kind,dtype,d,page,block", [
+    ("e4m3", torch.bfloat16, 128, 64, 64), ("int8", torch.bfloat16, 128, 128, 32), ("e4m3", torch.float32, 128, 128, 128),
+    ("int8", torch.float32, 64, 64, 4), ("e4m3", torch.float16, 64, 256, 256), ("int8", torch.float16, 128, 16, 16),
+    ("e4m3", torch.float32, 128, 256, 256), ("int8", torch.bfloat16, 64, 32, 8), ("e4m3", torch.float32, 64, 16, 1)])
+def test_append_whole_blocks(kind, dtype, d, page, block):
+    """Prompts of whole blocks, which the form for prompts takes without a
+    search: from a block's first row and from its middle, with values that are
+    not finite, with a row left out, one skipped, one outside the pool, and
+    with a head count that leaves warps without work."""
+    kc = _kc()
+    tile = max(64, block)
+    hkv = {64: 21, 128: 9, 256: 5}[tile]   # enough rows for that form, none a multiple of a CTA's
+    kv, new = [0, block // 2 + 1, 3 * block, 0], [2 * tile, 2 * tile + 17, 2 * tile + 1, 2 * tile + block // 2]
+    lens = [a + b for a, b in zip(kv, new)]
+    width = max(-(-n // page) for n in lens)
+    num = sum(-(-n // page) for n in lens) + 1
+    rows, _ = tables_for(lens, page, width, num, 7 * d + block)
+    cache = random_cache(kc, num, hkv, page, d, block, kind, block + 1)
+    slots = _slots(kv, new, rows, page)
+    t = len(slots)
+    g = torch.Generator().manual_seed(block + d)
+    x = torch.randn(t, 2, hkv, d, generator=g) * torch.exp2(torch.randint(-5, 6, (t, 2, hkv, 1), generator=g).float())
+    x[3, 0, ::2, 3] = float("inf")
+    x[tile + 5, 1, 1, 4] = float("-inf")
+    x[2 * tile + 70, :, 2] = float("nan")
+    x[block:2 * block, :, 3, :] = float("nan")
+    x[0:block, 1, 4, :] = 0.0
+    x = x.to(dtype).cuda()
+    ws = kc.Workspace(kc.Shape.make(1, 2, 2, 64, 1, 16), (kc.OP_DENSE,))
+    _append_and_check(cache, kind, x[:, 0], x[:, 1], slots, ws)
+    left = [i for i in range(t) if i not in (2, 4 * tile + 18)]   # blocks with a row that no token fills
+    fewer, y = [slots[i] for i in left], x[torch.tensor(left, device="cuda")] * 2
+    fewer[tile + 9] = -1
+    _append_and_check(cache, kind, y[:, 1], y[:, 0], fewer, ws)
+    assert ws.error() == 0
+    fewer[tile + 9] = num * page
+    _append_and_check(cache, kind, y[:, 0], y[:, 1], fewer, ws)
+    assert ws.error(clear=True) == kc.DEVERR_PAGE
+
+
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
 def test_append_values_at_the_edges(kind):
     """Zero blocks, infinities, NaN, the largest and smallest magnitudes, values

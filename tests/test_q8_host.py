@@ -177,6 +177,7 @@ def test_append_refusals():
     for bad in ((68, 64, 64, 64), (64, 66, 64, 64), (64, 64, 65, 64), (64, 64, 64, 4)):
         assert f(c, 256, 256, *bad, 0, 4, 256, None, 0, None) == kc.ERR_UNSUPPORTED
     assert f(c, 256, 256, 66, 64, 64, 64, 1, 4, 256, None, 0, None) == kc.ERR_UNSUPPORTED
+    assert f(c, 256, 256, 64, 64, 64, 64, 0, 1 << 30, 256, None, 0, None) == kc.ERR_UNSUPPORTED   # rows are numbered in 31 bits
 
 
 def test_gather_refusals():
