@@ -383,7 +383,8 @@ typedef struct kascade_q8_cache {
  * page_table entries; other entries are left as they were.
  *   kv_lens, new_lens  device int32 [batch], sums in [0, 2^20]
  *   free_pages   device int32 [num_free], pages no request holds
- *   page_table   device int32 [batch, max_pages], read and written
+ *   page_table   device int32 [batch, max_pages], read and written; apart from
+ *                the lengths
  *   kv_lens_out  device int32 [batch]: kv_lens + new_lens (a buffer that
  *                overlaps neither; copy it over kv_lens afterwards, or use
  *                the two in turn)

@@ -820,7 +820,7 @@ int kascade_page_tables(int32_t batch, int32_t page_size, int32_t max_pages, con
   };
   const int32_t* ins[] = {kv_lens, new_lens};
   for (const int32_t* in : ins)
-    if (overlap(kv_lens_out, batch, in, batch) || overlap(offsets, (int64_t)batch + 1, in, batch) ||
+    if (overlap(page_table, (int64_t)batch * max_pages, in, batch) || overlap(kv_lens_out, batch, in, batch) || overlap(offsets, (int64_t)batch + 1, in, batch) ||
         overlap(info, 2, in, batch) || (capacity && overlap(slot_map, capacity, in, batch)))
       return KASCADE_ERR_INVALID_ARG;
   PageTablesArgs a{};

@@ -228,7 +228,7 @@ def test_page_tables_refusals():
         return f(*[kw.get(n, v) for n, v in zip(names, ok)])
     for kw in (dict(batch=0), dict(width=0), dict(nfree=-1), dict(cap=-1), dict(kv=None), dict(new=None), dict(free=None),
                dict(table=None), dict(out=None), dict(off=None), dict(slots=None), dict(info=None),
-               dict(out=4096), dict(out=8192), dict(out=4108), dict(off=4096), dict(info=8192), dict(slots=4096 - 36)):
+               dict(out=4096), dict(out=8192), dict(table=8192), dict(kv=16384 + 4 * 31), dict(out=4108), dict(off=4096), dict(info=8192), dict(slots=4096 - 36)):
         assert but(**kw) == kc.ERR_INVALID_ARG, kw
     for kw in (dict(batch=4097), dict(page=48), dict(page=8), dict(page=8192), dict(kv=4098), dict(table=16386)):
         assert but(**kw) == kc.ERR_UNSUPPORTED, kw
