@@ -319,7 +319,7 @@ __device__ __forceinline__ uint4 requant16(uint4 y, float r) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// What both kernels know of their (kv head, tensor).
+// What the kernels know of their (kv head, tensor).
 template <int D, int IN, int CT>
 struct Appender {
   static constexpr int LPR = D / 8;           // lanes per input row
