@@ -255,9 +255,9 @@ struct MaxAcc {
 // where something was dropped): rounding that to at most 8 bits then gives
 // what rounding the exact value would, which a nearest fp32 value next to a
 // border does not.  (A remainder below fp32's range belongs to a value that
-// rounds to zero.)
+// rounds to zero; that of an infinity is NaN, which is no remainder.)
 __device__ __forceinline__ float odd_if(float y, float rest) {
-  return rest != 0.0f ? __uint_as_float(__float_as_uint(y) | 1u) : y;
+  return fabsf(rest) > 0.0f ? __uint_as_float(__float_as_uint(y) | 1u) : y;
 }
 __device__ __forceinline__ float mul_odd(float x, float s) {
   const float y = __fmul_rz(x, s);

@@ -1,0 +1,67 @@
+"""The append where a block keeps a scale of the caller's own, against the
+oracle: values, NaN and the signs of zeros."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import q8_oracle as Q
+from q8_cases import held, random_cache
+
+pytestmark = pytest.mark.gpu
+
+
+def _kc():
+    from sparse_attention_long_anchor_b200 import kascade as kc
+    return kc
+
+
+def _check(cache, kind, k, v, slots):
+    """Appends and compares: scales, values, places of NaN, and (e4m3 has a
+    negative zero) sign bits."""
+    want = [x.copy() for x in held(cache, kind)]
+    with np.errstate(invalid="ignore"):
+        for which, x in enumerate((k, v)):
+            Q.append(want[which], want[2], x.float().cpu().numpy(), list(slots), which, cache.scale_block, kind)
+    _kc().q8_append(cache, k, v, torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    got = held(cache, kind)
+    assert np.array_equal(got[2], want[2])
+    for a, b in zip(got[:2], want[:2]):
+        nan = np.isnan(b)
+        assert np.array_equal(np.isnan(a), nan)
+        assert np.array_equal(a[~nan], b[~nan])
+        if kind == "e4m3":
+            assert np.array_equal(np.signbit(a[~nan]), np.signbit(b[~nan]))
+
+
+# (kv heads, tokens, block): runs of up to eight rows and longer ones of the form for few tokens, and the form for
+# many (32 heads, more than 256 tokens), where a block is a tile of its own or one of several
+FORMS = [(2, 6, 64), (2, 40, 64), (32, 300, 64), (32, 300, 8), (32, 300, 256)]
+
+
+def _kept(kind, hkv, t, block, scale, dtype, spread, seed):
+    """t rows behind the first half block of a cache whose scales are all
+    `scale`: the first run continues that block and keeps it."""
+    kc = _kc()
+    d, page = 64, 256
+    cache = random_cache(kc, 4, hkv, page, d, block, kind, seed)
+    cache.scales.fill_(scale)
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(t, 2, hkv, d, generator=g) * spread
+    x[0, 0, :, 5] = float("inf")
+    x[1, :, 0, 6] = float("-inf")
+    x[2, 1, 1, :3] = float("nan")
+    x[3] = 0.0
+    x[4, :, :, 1::2] = -0.0
+    at = block // 2
+    slots = [page * (1 + (at + i) // page) + (at + i) % page for i in range(t)]   # pages 1, 2, ..
+    return cache, x.to(dtype).cuda(), slots
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hkv,t,block", FORMS)
+@pytest.mark.parametrize("scale", [0.3 * 2 ** 10, 0.7])
+def test_infinities_under_a_scale_that_is_no_power_of_two(kind, hkv, t, block, scale):
+    """Infinities saturate and NaN stays itself, as under a power of two."""
+    for dtype in (torch.bfloat16, torch.float32):
+        cache, x, slots = _kept(kind, hkv, t, block, scale, dtype, 3.0, t + block)
+        _check(cache, kind, x[:, 0], x[:, 1], slots)
