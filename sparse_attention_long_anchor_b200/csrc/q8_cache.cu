@@ -270,7 +270,8 @@ __device__ __forceinline__ float div_odd(float x, float s) {
 
 // rn(x / s).  For a power of two the product with 1 / s is the quotient; a
 // block that keeps a scale of the caller's own may have any other.
-__device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
+__device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }   // (infinity too)
+constexpr float kMaxEasy = 0x1p126f;   // the largest scale whose reciprocal is a normal number
 template <int IN, int CT>
 __device__ __forceinline__ uint2 pack8_pow2(const Raw8<IN>& r, float inv) {
   float x[8];
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(kTileThreads, 5)
                                                   // of a run, then its scale, as bits
   int* const sl = reinterpret_cast<int*>(run_top + kTileWarps * tile);   // [kLook + 2 tile] slots of tokens t0 - kLook ..
   __shared__ uint32_t lead[kMaxTile / 32];        // bit x: a run starts at token t0 + x
-  __shared__ int flags[kTileWarps][2];            // of a set: an infinity or NaN met; a scale that is no power of two
+  __shared__ int flags[kTileWarps][2];            // of a set: an infinity or NaN met; a scale that is not easy (below)
   __shared__ int end_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int mine = warp / wps, part = warp - mine * wps;   // the warp's set in the CTA, and its part of the rows
@@ -823,7 +824,7 @@ __global__ void __launch_bounds__(kTileThreads, 5)
     sync_set();
   }
   // scales, a lane per run; rows before a run whose scale grew, by the warp
-  bool pow2 = true;
+  bool easy = true;   // every scale's reciprocal is a normal power of two
   if (part == 0) {
     for (int x0 = 0; x0 < tile; x0 += 32) {
       const int x = x0 + lane;
@@ -838,7 +839,7 @@ __global__ void __launch_bounds__(kTileThreads, 5)
         const float s = ap.new_scale(top[r], offset, offset ? *sp : 0.0f, ratio);
         *sp = s;
         top[r] = __float_as_uint(s);
-        pow2 &= is_pow2(s);
+        easy &= is_pow2(s) && s <= kMaxEasy;
       }
       for (uint32_t grew = __ballot_sync(0xffffffffu, ratio != 1.0f); grew; grew &= grew - 1) {
         const int l = __ffs(grew) - 1;
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(kTileThreads, 5)
       }
     }
   }
-  if (any_of_set(!pow2, 1)) {
+  if (any_of_set(!easy, 1)) {
     for_rows([&](const Raw8<IN>& v, int x) {
       const uint32_t r = row_at(x);
       if (r != kNoRow) ap.store_row(r + head_row, v, __uint_as_float(top[run_of(x)]));
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(kTileThreads, 5)
 #pragma unroll 4
       for (int q = 0; q < n - 1; ++q, row += step) {
         const uint2 r = *row;
-        // 1 / s by its exponent: s = 2^e, |e| <= 122
+        // 1 / s by its exponent: s = 2^e, -100 <= e <= 126
         const float inv = __uint_as_float((254u << 23) - top[r.y]);
         *reinterpret_cast<uint2*>(pages + (size_t)r.x * D) = pack8_pow2<IN, CT>(kept_at(q), inv);
       }

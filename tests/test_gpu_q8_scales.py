@@ -65,3 +65,14 @@ def test_infinities_under_a_scale_that_is_no_power_of_two(kind, hkv, t, block, s
     for dtype in (torch.bfloat16, torch.float32):
         cache, x, slots = _kept(kind, hkv, t, block, scale, dtype, 3.0, t + block)
         _check(cache, kind, x[:, 0], x[:, 1], slots)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hkv,t,block", FORMS)
+@pytest.mark.parametrize("scale", [2.0 ** 122, 2.0 ** 123, 2.0 ** 126, 2.0 ** 127, 1.7 * 2.0 ** 127, float("inf")])
+def test_scales_past_those_that_the_append_writes(kind, hkv, t, block, scale):
+    """x / s for scales up to fp32's largest, whose reciprocals are below its
+    normal range, and for an infinite one (zeros, and NaN for infinities)."""
+    for dtype in (torch.bfloat16, torch.float32):
+        cache, x, slots = _kept(kind, hkv, t, block, scale, dtype, 2.0 ** 124, t + block + 1)
+        _check(cache, kind, x[:, 0], x[:, 1], slots)
