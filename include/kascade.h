@@ -394,6 +394,10 @@ typedef struct kascade_q8_cache {
  *                every new token, requests in order, positions ascending;
  *                -1 from the total on (a fixed capacity serves a graph)
  *   info         device int32 [2]: pages taken, new tokens
+ * The call knows no pool.  An entry of page_table or free_pages that no pool
+ * can have (negative, or with slots past 2^31 - 1) gives its tokens the slot
+ * -2^31, one outside the pool in use a slot outside it: kascade_q8_append
+ * skips and reports both.
  * All or nothing: a negative length, a request past max_pages pages or 2^20
  * tokens, more than num_free pages or more than capacity tokens make the call
  * give info = (-1, 0), kv_lens_out = kv_lens, offsets 0 and every slot -1, and

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const PageTabl
           page_of = pi;
           page_b = b;
         }
-        out[u] = (int)(((unsigned)page << a.page_shift) | (unsigned)(pos & P1));
+        out[u] = q8_slot(page, (uint32_t)(pos & P1), a.page_shift);
       }
     }
     if (t0 + kTabTokens <= a.capacity && (((uintptr_t)a.slot_map) & 15) == 0) {

@@ -32,6 +32,14 @@ Q8_HD bool q8_slot_ok(int32_t slot, int32_t num_pages, int page_shift) {
   return (uint32_t)slot < ((uint32_t)num_pages << page_shift);
 }
 
+// Slot of row `in_page` of the page that a table or free-list entry names.  No
+// pool has a page whose slots pass 31 bits, or a negative one: kBadSlot stands
+// for their rows, which lies in no pool either and is not the padding mark.
+constexpr int32_t kBadSlot = -2147483647 - 1;
+Q8_HD int32_t q8_slot(int32_t entry, uint32_t in_page, int page_shift) {
+  return (uint32_t)entry <= 0x7fffffffu >> page_shift ? (int32_t)((uint32_t)entry << page_shift | in_page) : kBadSlot;
+}
+
 // Row of kv head h at row `in_page` of `page`: below num_pages Hkv P < 2^31.
 Q8_HD uint32_t q8_row(uint32_t page, uint32_t in_page, uint32_t h, uint32_t Hkv, int page_shift) {
   return ((page * Hkv + h) << page_shift) + in_page;
