@@ -852,6 +852,9 @@ int kascade_q8_append(const kascade_q8_cache* c, const void* k, const void* v, i
   if (num_tokens == 0) return KASCADE_OK;
   if (!k || !v || !slot_map) return KASCADE_ERR_INVALID_ARG;
   const int64_t unit = dtype == KASCADE_DTYPE_F32 ? 4 : 8;   // elements of 16 bytes
+  // a dimension of one element has no stride
+  if (num_tokens == 1) k_token_stride = v_token_stride = 0;
+  if (c->num_kv_heads == 1) k_head_stride = v_head_stride = 0;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4) || k_token_stride % unit || k_head_stride % unit ||
       v_token_stride % unit || v_head_stride % unit)
     return KASCADE_ERR_UNSUPPORTED;
