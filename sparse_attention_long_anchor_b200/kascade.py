@@ -487,12 +487,15 @@ def q8_append(cache: Q8Cache, k, v, slot_map, ws=None, stream=None):
         _need(dev >= 0, where)
         with _on(cache.device, stream, where):
             return q8_append(cache, k, v, slot_map, ws)
-    t = k.shape[0]
-    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
     dtype = k.dtype
-    if (k.shape != (t, cache.num_kv_heads, cache.head_dim) or v.shape != k.shape or v.dtype is not dtype
-            or dtype not in _DTYPES or k.get_device() != dev or v.get_device() != dev):
+    shape = k.shape
+    if (len(shape) != 3 or v.shape != shape or v.dtype is not dtype or dtype not in _DTYPES
+            or k.get_device() != dev or v.get_device() != dev):
         raise KascadeError(ERR_INVALID_ARG, where)
+    t, heads, d = shape
+    if heads != cache.num_kv_heads or d != cache.head_dim:
+        raise KascadeError(ERR_INVALID_ARG, where)
+    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
     _need(kd == 1 and vd == 1, where, ERR_UNSUPPORTED)
     p, n = ws.args() if ws is not None else (None, 0)
     status = lib.kascade_q8_append(cache.ref, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, _DTYPES[dtype], t,

@@ -33,3 +33,17 @@ def test_strides_of_dimensions_of_one_do_not_matter(dtype, t, hkv):
     with pytest.raises(kc.KascadeError):
         y = torch.zeros(4, hkv, d + 1, dtype=dtype, device="cuda")[..., :d]
         kc.q8_append(caches[0], y, y, _slots([1, 2, 3, 4]))
+
+
+def test_rows_of_another_rank_are_refused():
+    """As every other wrong argument is: by the binding's own error."""
+    kc = _kc()
+    cache = random_cache(kc, 3, 2, 16, 64, 4, "e4m3", 7)
+    before = raw(cache.k_pages).copy()
+    x = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    slots = _slots([0, 1, 2, 3, 4])
+    for k, v in ((x.view(5, 128), x.view(5, 128)), (x[None], x[None]), (x[0, 0], x[0, 0]), (x, x[None]), (x[None], x),
+                 (x.sum(), x.sum())):
+        with pytest.raises(kc.KascadeError):
+            kc.q8_append(cache, k, v, slots)
+    assert (raw(cache.k_pages) == before).all()
