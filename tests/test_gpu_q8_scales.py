@@ -76,3 +76,24 @@ def test_scales_past_those_that_the_append_writes(kind, hkv, t, block, scale):
     for dtype in (torch.bfloat16, torch.float32):
         cache, x, slots = _kept(kind, hkv, t, block, scale, dtype, 2.0 ** 124, t + block + 1)
         _check(cache, kind, x[:, 0], x[:, 1], slots)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("hkv,t,block", FORMS + [(2, 20, 1)])
+def test_signs_of_values_that_round_to_zero(dtype, hkv, t, block):
+    """Small values beside large ones, new ones and rows that a growing scale
+    rounds again: a negative one becomes e4m3's negative zero."""
+    kc = _kc()
+    d, page = 64, 256
+    cache = random_cache(kc, 4, hkv, page, d, block, "e4m3", t)
+    g = torch.Generator().manual_seed(t + block)
+    x = torch.randn(t, 2, hkv, d, generator=g)
+    x[:, :, :, 1::4] *= 2.0 ** -14    # below half of the smallest value, 2^-10, at scales from 2^-8 up
+    x[:, :, :, 2] = -0.0
+    x *= 2.0 ** 13                    # old rows of size 1 fall below 2^-10 at the new scales
+    at = block // 2
+    slots = [page * (1 + (at + i) // page) + (at + i) % page for i in range(t)]
+    x = x.to(dtype).cuda()
+    _check(cache, "e4m3", x[:, 0], x[:, 1], slots)
+    k = held(cache, "e4m3")[0]
+    assert ((k == 0) & np.signbit(k)).any()
