@@ -350,7 +350,7 @@ KASCADE_API int kascade_sparse_decode_paged(const kascade_shape* shape, const vo
  *             (K scale, V scale) of scale_block consecutive rows of a page and
  *             kv head; a stored value stands for itself times its scale.  The
  *             calls read any scale; kascade_q8_append writes powers of two
- *             in [2^-100, 2^122]
+ *             in [2^-100, 2^122], or keeps a larger one that it finds
  *   page_size a power of two in [16, 4096]; scale_block a power of two in
  *             [1, min(page_size, 256)]; num_pages Hkv page_size < 2^31
  *
@@ -422,7 +422,9 @@ KASCADE_API int kascade_page_tables(int32_t batch, int32_t page_size, int32_t ma
  * 448 or 127), and not less than the block's scale if rows precede; where it
  * grows, those rows are rounded again at the new scale.  A new value is
  * x / s rounded to nearest, ties to even, saturated at +-M (infinities too); NaN
- * is e4m3's NaN, and 0 in int8.
+ * is e4m3's NaN, and 0 in int8.  (A block's scale that is NaN counts for
+ * nothing: the bytes before stay.  An infinite one is kept: x / s is 0, and NaN
+ * for infinities.)
  *   dtype  KASCADE_DTYPE_* of k and v
  *   ws     NULL, or a workspace whose error word takes bad slots
  */
@@ -462,6 +464,8 @@ KASCADE_API int kascade_q8_gather(const kascade_q8_cache* cache, int32_t batch, 
  * after the kascade_q8_append of the same layer).
  * The V scales of the keys that one row attends over should lie within a
  * factor of 2^24 of one another: values of blocks below that keep fewer bits.
+ * (Weights times V scales are rounded to fp16, 2^-11 relative; scores, sums and
+ * accumulators are fp32.)
  */
 KASCADE_API int kascade_sparse_decode_q8(const kascade_shape* shape, const kascade_q8_cache* cache, const void* q,
                                          const int32_t* page_table, int32_t max_pages, const int32_t* kv_lens,

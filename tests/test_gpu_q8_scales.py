@@ -97,3 +97,30 @@ def test_signs_of_values_that_round_to_zero(dtype, hkv, t, block):
     _check(cache, "e4m3", x[:, 0], x[:, 1], slots)
     k = held(cache, "e4m3")[0]
     assert ((k == 0) & np.signbit(k)).any()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hkv,t,block", FORMS)
+def test_a_scale_that_is_nan_counts_for_nothing(kind, hkv, t, block):
+    """The new rows take the scale that they alone would; the bytes before them
+    stay."""
+    kc = _kc()
+    d, page, at = 64, 256, block // 2
+    caches = [random_cache(kc, 4, hkv, page, d, block, kind, t) for _ in range(2)]
+    caches[0].scales.fill_(float("nan"))
+    caches[1].scales.fill_(2.0 ** -100)
+    for c in caches:   # (zeros: rounding them again at another scale keeps them)
+        for p in (c.k_pages, c.v_pages):
+            p.view(torch.uint8)[1, :, :at] = 0
+    caches[0].k_pages.view(torch.uint8)[1, :, :at] = 3
+    x = torch.randn(t, 2, hkv, d, generator=torch.Generator().manual_seed(t + block)).bfloat16().cuda()
+    slots = torch.tensor([page * (1 + (at + i) // page) + (at + i) % page for i in range(t)], dtype=torch.int32, device="cuda")
+    for c in caches:
+        kc.q8_append(c, x[:, 0], x[:, 1], slots)
+    got, want = [held(c, kind) for c in caches]
+    written = ~np.isnan(got[2])
+    assert written.any() and np.array_equal(got[2][written], want[2][written])
+    assert (caches[0].k_pages.view(torch.uint8)[1, :, :at] == 3).all()
+    assert (caches[0].v_pages.view(torch.uint8)[1, :, :at] == 0).all()
+    got[0][1, :, :at] = 0
+    assert np.array_equal(got[0], want[0], equal_nan=True) and np.array_equal(got[1], want[1], equal_nan=True)
