@@ -16,8 +16,8 @@ namespace {
 // prefix sums of m and need, the call writes page_table[b, first_b + i] =
 // free[f_b + i] and the slots of b's new tokens at slot_map[c_b ...].
 //
-// Bound by latency (a few dependent loads), not by its bytes: 3.3 us for a step
-// of 8 requests, 8.1 us for 2048 requests and a million slots.  Each CTA
+// Bound by latency (a few dependent loads), not by its bytes: 3.4 us for a step
+// of 8 requests, 8.2 us for 2048 requests and a million slots.  Each CTA
 // computes the prefix sums of all requests for itself (2 B integers out of L2)
 // and then writes its share of the slots, the new table entries and the
 // lengths: one launch, no exchange between CTAs.  That is why lens_out must not
@@ -147,9 +147,9 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const PageTabl
 //   grew, those rows become rn(y s_old / s);
 //   the new rows become rn(x / s).
 // Bound by HBM for prompts: each input value is read once and waits on the SM
-// for its run's maximum, each byte is written once: 36 us for a 32K prompt of 8
-// kv heads, d = 128 in bf16 (5.6 TB/s), 58 us in fp32 (5.8 TB/s).  A decode
-// step is bound by latency: 2.2 us for 8 requests.
+// for its run's maximum, each byte is written once: 36.6 us for a 32K prompt of 8
+// kv heads, d = 128, blocks of 64 in bf16 (5.5 TB/s), 58 us in fp32 (5.8 TB/s).  A
+// decode step is bound by latency: 2.5 us for 8 requests.
 //
 // Three kernels, by the block's size and the number of tokens (see run_append).
 // The heads of a token are worked on next to one another: together they read
@@ -161,7 +161,11 @@ constexpr int kMaxTile = 256;
 // CTAs of the form for few tokens (8 tokens of a set each) up to which it is
 // taken.  8 kv heads, d = 128 in bf16, few against many: decode steps of 512
 // 6.0 and 14.5 us, of 1024 9.9 and 14.4, of 2048 17.7 and 14.6; prompts of 1000
-// tokens 7.7 and 7.1, of 2048 12.0 and 4.4 (8 of 250 13.4 and 13.5).
+// tokens 7.7 and 7.1, of 2048 12.0 and 4.4 (8 of 250 13.4 and 13.5).  13 ragged
+// chunks of d = 64 in fp32, blocks of 16, where the form for many takes 10 us
+// whatever their length: 1392 CTAs 7.3 and 10.0 us, 1808 8.0 and 10.2, 3148
+// 10.7 and 10.6, 4024 12.8 and 10.3; one prompt of those rows, 1024 CTAs 5.9 and
+// 5.8, 2000 8.0 and 7.4, 4096 13.3 and 6.6.
 constexpr int kFewCtas = 2048;
 constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr int kLook = 32;      // skipped tokens that part two runs of one block
@@ -965,7 +969,10 @@ cudaError_t run_append(const Q8AppendArgs& a, cudaStream_t st) {
   if (few <= kFewCtas)
     return launch_ex(q8_append_kernel<D, IN, CT>, dim3((unsigned)few), dim3(kAppThreads), 0, st, false, 1, a);
   // as many warps to a (head, tensor) as hold a tile's rows: a block's where a
-  // run is a tile, else the tile's and those of a run that reaches over its end
+  // run is a tile, else the tile's and those of a run that reaches over its end.
+  // (128 KB of rows, as in fp32 blocks of 256 at d = 128, are twice what the four
+  // hold: they come in two chunks, one of them twice, and never as whole blocks.
+  // 32K tokens of 8 kv heads take 89 us then, and 62 in blocks of 128.)
   constexpr int ROW = D * (IN == kInF32 ? 4 : 2), PASS = IN == kInF32 ? 1024 : 512;   // bytes of a row, and a warp's pass
   const int block = 1 << a.c.block_shift, tile = min(max(block, 64), kMaxTile);
   const int window = (block >= tile ? tile : tile + block) * ROW;

@@ -22,11 +22,14 @@
 // Bytes widen to fp16, which holds every e4m3 and int8 value exactly.  The two
 // other operands are brought into fp16's range without giving up bits:
 //   * q is scaled per head by a power of two to a largest magnitude in
-//     [2^14, 2^15); bf16's 8 bits (fp16's 11) then stay exact down to 2^-28
-//     (2^-25) of that magnitude, smaller ones lose at most 2^-40 of it;
+//     [2^14, 2^15); bf16's 8 bits (fp16's 11) then stay exact down to 2^-31
+//     (2^-28) of that magnitude, smaller ones lose at most half of fp16's
+//     smallest step, 2^-25, which is 2^-39 of it;
 //   * p vs (p <= 1) is scaled by 2^(14 - E), E the largest exponent of vs that
 //     the warp has met (the accumulators are rescaled when it grows, as they
-//     are for the running maximum), and rounds to fp16: 2^-12 relative.
+//     are for the running maximum), and rounds to fp16: by 2^-11 of itself, or,
+//     where that is more (products below fp16's normal range), by 2^-25 in
+//     units of 2^(E - 14).
 // Scores, softmax statistics and accumulators are fp32.
 //
 // Three ways to split the work, by the problems' number and length (see run);
@@ -455,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
   }
   // q as B operand of S^T, scaled into fp16.  It is kept in shared memory, the
   // same for every warp: registers are short (128 a thread) and the four reads
-  // a tile cost less (Llama-shaped 32K lists 7.75 -> 7.6 us, dense 101 -> 100).
+  // a tile cost less (Llama-shaped 32K lists, rows in L2, 7.75 -> 7.6 us; dense 101
+  // -> 100).
   uint4* qs = reinterpret_cast<uint4*>(smem + L::q) + lane;
   float sc0, sc1;   // score scale of heads 2c and 2c + 1: log2(e) / sqrt(D) and q's power of two
   {
