@@ -412,11 +412,11 @@ KASCADE_API int kascade_page_tables(int32_t batch, int32_t page_size, int32_t ma
  * Quantises new K and V rows into the cache.  Token t's rows, kv head h, are
  * k + t k_token_stride + h k_head_stride (elements; strides are whole 16-byte
  * units, so views of a fused projection serve; the stride of a single token or
- * head does not matter) and go to slot slot_map[t]; slot -1 skips the token.  Tokens of one block must be neighbours in the
- * token order (up to 31 skipped ones between two of them do not matter), their
- * slots ascending and distinct, as kascade_page_tables writes them; the rows
- * of the block before the first of them are in use, those behind the last are
- * not.
+ * head does not matter) and go to slot slot_map[t]; slot -1 skips the token.
+ * Tokens of one block must be neighbours in the token order (up to 31 skipped
+ * ones between two of them do not matter), their slots ascending and distinct,
+ * as kascade_page_tables writes them; the rows of the block before the first
+ * of them are in use, those behind the last are not.
  * For the new rows x of a block (per kv head, K and V apart), a the largest
  * finite |x|: the scale becomes the smallest power of two s with a <= M s (M =
  * 448 or 127), and not less than the block's scale if rows precede; where it
