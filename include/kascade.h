@@ -449,7 +449,8 @@ KASCADE_API int kascade_q8_gather(const kascade_q8_cache* cache, int32_t batch, 
  * kascade_sparse_decode over the 8-bit paged cache: the attention of q over
  * the values that the cache stands for.
  *   kv_lens  device int32 [B], held to [0, N] (NULL: N each); a row of 0 keys
- *            gives o = 0, lse = -inf
+ *            gives o = 0, lse = -inf.  (A key whose score is -inf has no
+ *            weight; a row of such keys alone gives o = NaN, lse = -inf.)
  *   idx      lists in the layout of kv_len = N, as kascade_select_varlen
  *            writes them (row b's first ceil(frac kv_lens[b]) entries are
  *            read, in any order), or NULL for dense decode over the row's keys

@@ -150,6 +150,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// A running maximum starts at kNoScore, so that scores of minus infinity weigh
+// ex2(-inf) = 0 whatever comes before them; it is -inf where there was no key.
+constexpr float kNoScore = -3.402823466e+38f;   // fp32's lowest
 // weight of a partial result with running maximum m when joined at M
 __device__ __forceinline__ float join_weight(float m, float M) { return m == -INFINITY ? 0.0f : ex2_fast(m - M); }
 
@@ -249,8 +252,8 @@ __device__ __forceinline__ bool part_of_cta(const Q8DecodeArgs& a, int mine, int
 
 // four consecutive outputs, normalised and rounded once
 template <int QT>
-__device__ __forceinline__ void store_out(const Q8DecodeArgs& a, size_t at, float4 x, float l) {
-  const float inv = l == 0.f ? 0.f : 1.0f / l;   // no key: zero
+__device__ __forceinline__ void store_out(const Q8DecodeArgs& a, size_t at, float4 x, float M, float l) {
+  const float inv = M == -INFINITY ? 0.f : 1.0f / l;   // no key: zero (none but weights of zero: 0 / 0)
   uint32_t lo, hi;
   if constexpr (QT == kInBf16) {
     lo = pack_bf16(x.x * inv, x.y * inv), hi = pack_bf16(x.z * inv, x.w * inv);
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
   }
   __syncthreads();
 
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // heads 2c, 2c + 1; sums over this lane's keys
+  float m0 = t0 < t_end ? kNoScore : -INFINITY, m1 = m0, l0 = 0.f, l1 = 0.f;   // heads 2c, 2c + 1; sums over this lane's keys
   int e_run = 27;                                             // biased exponent E of the V scales met so far
   float oacc[MT][4];   // tile t: dim g D/8 + 2t of heads 2c, 2c + 1, then dim g D/8 + 2t + 1
 #pragma unroll
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
   if constexpr (kCluster) {
     if (cs == 1) {
       if (hh < G) {
-        store_out<QT>(a, orow * D + d4, acc, l);
+        store_out<QT>(a, orow * D + d4, acc, M, l);
         if (d4 == 0 && a.lse) a.lse[orow] = lse_of(M, l);
       }
       return;
@@ -704,14 +707,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) q8_decode_kernel(const Q
     }
     if (have && r == 0) {
       const size_t row = (size_t)b * a.Hq + h * G + uh;
-      store_out<QT>(a, row * D + ud, acc, l);
+      store_out<QT>(a, row * D + ud, acc, M, l);
       if (ud == 0 && a.lse) a.lse[row] = lse_of(M, l);
     }
     return;
   }
   if (hh < G) {
     if (ta == 0 && tb == tiles_b) {   // the problem whole
-      store_out<QT>(a, orow * D + d4, acc, l);
+      store_out<QT>(a, orow * D + d4, acc, M, l);
       if (d4 == 0 && a.lse) a.lse[orow] = lse_of(M, l);
     } else {
       const size_t pr = (size_t)blockIdx.x * G + hh;
@@ -742,7 +745,7 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(const Q8DecodeArg
   const int mine = a.per > 0 || !a.kv_lens ? 0 : first_rows(a);
   const int tiles = row_tiles(a, b);
   if (tiles == 0) {   // no key: zeros (no CTA above had this problem)
-    if (grp == 0) store_out<QT>(a, orow * D + d4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+    if (grp == 0) store_out<QT>(a, orow * D + d4, make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
     if (tid == 0 && a.lse) a.lse[orow] = -INFINITY;
     return;
   }
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(const Q8DecodeArg
     l += f * ml.y;
     acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
   }
-  store_out<QT>(a, orow * D + d4, acc, l);
+  store_out<QT>(a, orow * D + d4, acc, M, l);
   if (d4 == 0 && a.lse) a.lse[orow] = lse_of(M, l);
 }
 
